@@ -346,6 +346,194 @@ mx_status mx_linear_batched(int32_t op, int32_t count, const mx_qtensor *A, cons
  */
 mx_status mx_dequantize(const mx_qtensor *q, float *out, int64_t ld, void *stream);
 
+/*
+ * RMS norm of a residual stream into packed operands: what stands between two
+ * quantized linears of a transformer layer, in one call.
+ *     h    = x + residual                       (rounded to `dtype`)
+ *     rstd = 1 / sqrt(mean_k h_k^2 + eps)       (64-bit sum, rounded to fp32)
+ *     y    = (h * rstd) * weight                (fp32)
+ * y is then rotated, scaled and rounded as mx_quantize does with its source,
+ * except that y enters in fp32: it is never rounded to bf16 and never written.
+ *
+ *  x          device [rows, cols], leading dimension ldx (elements), `dtype`.
+ *  residual   device [rows, cols], ldr, or NULL for none. Without it h is x
+ *             and the fields h and ldh are not read.
+ *  h          device [rows, cols], ldh. Written. May be x or residual itself
+ *             (same pointer and leading dimension); must not overlap them
+ *             otherwise.
+ *  weight     device [cols], `weight_dtype`.
+ *  rstd       device fp32 [rows]. Written; mx_rmsnorm_backward reads it.
+ *  dtype, weight_dtype   mx_out_dtype: MX_OUT_F32 or MX_OUT_BF16.
+ *  eps        >= 0 and finite.
+ * x, residual, h, weight: 16-byte aligned; leading dimensions >= cols and a
+ * multiple of 16 bytes (8 bf16 or 4 fp32 elements); rstd: 4-byte aligned.
+ */
+typedef struct mx_norm {
+  const void *x, *residual;
+  const void *weight;
+  void *h;
+  float *rstd;
+  int64_t rows, cols;
+  int64_t ldx, ldr, ldh;
+  int32_t dtype, weight_dtype;
+  double eps;
+} mx_norm;
+
+/*
+ *  format     mx_format of the operands.
+ *  block, rotate, round, seed1, seed0: as for mx_quantize_dual (seed1 for the
+ *             axis-1 operand, seed0 for the axis-0 one); MX_FMT_FP8_E4M3 takes
+ *             MX_ROUND_RNE only.
+ *  codes1, scales1, desc1: the axis-1 operand of y, sizes from
+ *             mx_quantize_sizes (mx_quantize_fp8_sizes), written in full.
+ *  codes0, scales0, desc0: the axis-0 operand, or codes0 == scales0 == NULL
+ *             for none (desc0 is then not written).
+ * Requirements: cols % 32 == 0; with an axis-0 operand rows % 32 == 0. The
+ * operands' alignment and limits are mx_quantize's. rows == 0 or cols == 0
+ * launches nothing.
+ * A row that holds a NaN has rstd NaN and only 0xFF scales along the row; a
+ * row that holds an infinity has rstd 0 and a 0xFF scale where the infinity
+ * is (as NaN and infinity blocks of mx_quantize).
+ * Errors: MX_ERR_NULL, MX_ERR_ARG, MX_ERR_SHAPE, MX_ERR_ALIGN,
+ * MX_ERR_UNSUPPORTED, MX_ERR_HIP.
+ */
+mx_status mx_rmsnorm_quantize(const mx_norm *n, int32_t format, int32_t block, int32_t rotate,
+                              int32_t round, uint64_t seed1, uint64_t seed0, void *codes1,
+                              void *scales1, void *codes0, void *scales0, mx_qtensor *desc1,
+                              mx_qtensor *desc0, void *stream);
+
+/*
+ * Gradient of mx_rmsnorm_quantize (the quantization passes it through
+ * unchanged). With x^ = h * rstd:
+ *     dh      = rstd * (dy * weight - x^ * mean_k(dy * weight * x^)) + dres
+ *     dweight = sum over rows of dy * x^
+ * dh is the gradient of the stream h, and so of both x and residual.
+ *
+ *  dy         device [rows, cols], lddy: the gradient of y (the Dgrad outputs
+ *             of the linears that read it, added up).
+ *  h, rstd    what the forward call wrote (or its x, without a residual).
+ *  dres       device [rows, cols], ldres: the gradient that reaches h past the
+ *             norm, or NULL for none.
+ *  dh         device [rows, cols], lddh. Written. May be dy or dres itself
+ *             (same pointer and leading dimension); must not overlap the
+ *             inputs otherwise.
+ *  dweight    device fp32 [cols], 16-byte aligned. Written.
+ *  dtype      of dy, h, dres and dh; weight_dtype of weight.
+ * Alignment and leading dimensions as for mx_norm; rstd 4-byte aligned.
+ */
+typedef struct mx_norm_grad {
+  const void *dy, *h, *dres;
+  const float *rstd;
+  const void *weight;
+  void *dh;
+  float *dweight;
+  int64_t rows, cols;
+  int64_t lddy, ldh, ldres, lddh;
+  int32_t dtype, weight_dtype;
+} mx_norm_grad;
+
+/*
+ * Bytes of the workspace of mx_rmsnorm_backward. Host-only.
+ * Errors: MX_ERR_NULL, MX_ERR_SHAPE, MX_ERR_UNSUPPORTED (extents above 2^31).
+ */
+mx_status mx_rmsnorm_backward_workspace(int64_t rows, int64_t cols, size_t *bytes);
+
+/*
+ *  workspace  device, >= the bytes above, 16-byte aligned; its contents do not
+ *             matter before and are undefined after. Two calls that may run at
+ *             the same time need one each, and so do two captured graphs.
+ * Requirements: cols % 8 == 0. rows == 0 writes zeros to dweight; cols == 0
+ * launches nothing.
+ * Errors: MX_ERR_NULL, MX_ERR_ARG, MX_ERR_SHAPE (also a workspace that is too
+ * small), MX_ERR_ALIGN, MX_ERR_UNSUPPORTED, MX_ERR_HIP.
+ */
+mx_status mx_rmsnorm_backward(const mx_norm_grad *g, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/*
+ * One gradient tensor of a set: [rows, cols] with leading dimension ld
+ * (elements; ld == cols or rows <= 1: no gaps). Any element-aligned address.
+ */
+typedef struct mx_grad {
+  void *data;
+  int64_t rows, cols, ld;
+  int32_t dtype;        /* mx_out_dtype */
+} mx_grad;
+
+/*
+ * A set of gradient tensors, laid out once for the calls below.
+ *  grads, count  the host array it was made from, and
+ *  host_table    the host table that mx_grad_set_fill wrote (both BORROWED:
+ *                they must live, unchanged, as long as the set).
+ *  table         device copy of host_table; the caller uploads it
+ *                (table_bytes, 8-byte aligned) and sets this field.
+ *  chunks, chunk how the elements are cut up (set by mx_grad_set_fill).
+ */
+typedef struct mx_grad_set {
+  const mx_grad *grads;
+  int32_t count;
+  const void *host_table;
+  void *table;
+  size_t table_bytes;
+  int64_t chunks, chunk;
+} mx_grad_set;
+
+/*
+ * Bytes of a set's table. Host-only; launches nothing. Errors as for
+ * mx_grad_set_fill, which alone looks for memory given twice.
+ */
+mx_status mx_grad_set_size(int32_t count, const mx_grad *grads, size_t *table_bytes);
+
+/*
+ * Fill a set (all fields but `table`) and its table in HOST memory. Tensors
+ * may be empty. The table holds the tensors' addresses: a tensor that moves
+ * needs a new set.
+ *  host_table  >= table_bytes, 8-byte aligned.
+ * Errors: MX_ERR_NULL, MX_ERR_ARG (dtype, count < 0, the same memory twice: a
+ * tensor without gaps that overlaps another such, or a tensor with gaps that
+ * is given twice), MX_ERR_SHAPE (negative extents, ld < cols), MX_ERR_ALIGN
+ * (data not aligned to its elements), MX_ERR_UNSUPPORTED (more than 2^31
+ * chunks, or a tensor's span above 2^62 bytes).
+ */
+mx_status mx_grad_set_fill(int32_t count, const mx_grad *grads, void *host_table,
+                           size_t table_bytes, mx_grad_set *set);
+
+/* Bytes of the workspace of mx_grad_norm and mx_grad_clip. Host-only. */
+size_t mx_grad_workspace(void);
+
+/*
+ * Global 2-norm of a set: norm[0] = sqrt(sum g^2), squares and sums in 64
+ * bits, rounded to fp32 (so no square overflows or vanishes). 0 for a set
+ * without elements; NaN or infinity where an element is.
+ *  norm       device fp32. Written.
+ *  workspace  device, >= mx_grad_workspace() bytes, 8-byte aligned; as for
+ *             mx_rmsnorm_backward.
+ * Errors: MX_ERR_NULL, MX_ERR_SHAPE (a workspace that is too small),
+ * MX_ERR_ALIGN, MX_ERR_HIP.
+ */
+mx_status mx_grad_norm(const mx_grad_set *set, float *norm, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+/*
+ * Clipping by the global norm: with the norm of `in` as above and
+ * coef = min(1, max_norm / (norm + 1e-6)),
+ *     out = in * coef      (rounded to the tensor's type)
+ *     norm[0] = the norm before clipping
+ * `out` is a set of the same shapes and types as `in`, or `in` itself (the same
+ * set, or NULL) to clip in place; in place nothing is written while the norm is
+ * within max_norm. A tensor of `out` is the tensor of `in` at the same place of
+ * its set, or shares no memory with any of them (refused where both have no
+ * gaps, the caller's to see to where one has).
+ * A NaN norm makes every element NaN; an infinite one turns finite elements
+ * into zeros and infinite ones into NaN (norm tells).
+ *  max_norm   >= 0 (infinity: scale nothing).
+ * Errors: as for mx_grad_norm, and MX_ERR_ARG (max_norm negative or NaN, or
+ * memory shared between the sets as above), MX_ERR_MISMATCH (`out` of other
+ * shapes or types).
+ */
+mx_status mx_grad_clip(const mx_grad_set *in, const mx_grad_set *out, float max_norm, float *norm,
+                       void *workspace, size_t workspace_bytes, void *stream);
+
 /* Static, NUL-terminated name of a status code. Never NULL. */
 const char *mx_status_string(int32_t status);
 

@@ -14,18 +14,25 @@ durchbricht die bestehende Erkenntnis ...", section "Fehlerdiagnoseexperiment"):
     fprop: A = X  [T, in]  axis 1, B = W [out, in] axis 1 -> Y  [T, out]
     dgrad: A = dY [T, out] axis 1, B = W [out, in] axis 0 -> dX [T, in]
     wgrad: A = dY [T, out] axis 0, B = X [T, in]   axis 0 -> dW [out, in]
+
+Around the linears of a training step: rmsnorm_quantize writes the packed
+operands of the normalised residual stream, rmsnorm_backward is its gradient,
+and clip_grad_norm scales the gradients by their global norm.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 __all__ = [
     "LIB_PATH", "MxError", "QTensorDesc", "QTensor", "load_library", "library_symbols",
     "status_string", "version", "last_hip_error", "quantize_sizes", "quantize", "quantize_dual",
     "quantize_pair",
     "quantize_fp8_sizes", "quantize_fp8", "linear", "linear_batched", "dequantize",
+    "NormDesc", "NormGradDesc", "GradDesc", "GradSetDesc", "RMSNormQuantized",
+    "rmsnorm_quantize", "rmsnorm_backward", "GradSet", "grad_norm", "clip_grad_norm",
     "ROTATE", "ROUND", "FORMATS", "OPS", "OUT_DTYPES", "OP_AXES",
 ]
 
@@ -64,6 +71,70 @@ class QTensorDesc(ctypes.Structure):
         ("round", ctypes.c_int32),
         ("seed", ctypes.c_uint64),
         ("format", ctypes.c_int32),
+    ]
+
+
+class NormDesc(ctypes.Structure):
+    """Mirror of struct mx_norm in include/mxfp4.h."""
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("residual", ctypes.c_void_p),
+        ("weight", ctypes.c_void_p),
+        ("h", ctypes.c_void_p),
+        ("rstd", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("ldx", ctypes.c_int64),
+        ("ldr", ctypes.c_int64),
+        ("ldh", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("weight_dtype", ctypes.c_int32),
+        ("eps", ctypes.c_double),
+    ]
+
+
+class NormGradDesc(ctypes.Structure):
+    """Mirror of struct mx_norm_grad in include/mxfp4.h."""
+    _fields_ = [
+        ("dy", ctypes.c_void_p),
+        ("h", ctypes.c_void_p),
+        ("dres", ctypes.c_void_p),
+        ("rstd", ctypes.c_void_p),
+        ("weight", ctypes.c_void_p),
+        ("dh", ctypes.c_void_p),
+        ("dweight", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("lddy", ctypes.c_int64),
+        ("ldh", ctypes.c_int64),
+        ("ldres", ctypes.c_int64),
+        ("lddh", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("weight_dtype", ctypes.c_int32),
+    ]
+
+
+class GradDesc(ctypes.Structure):
+    """Mirror of struct mx_grad in include/mxfp4.h."""
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("ld", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class GradSetDesc(ctypes.Structure):
+    """Mirror of struct mx_grad_set in include/mxfp4.h."""
+    _fields_ = [
+        ("grads", ctypes.POINTER(GradDesc)),
+        ("count", ctypes.c_int32),
+        ("host_table", ctypes.c_void_p),
+        ("table", ctypes.c_void_p),
+        ("table_bytes", ctypes.c_size_t),
+        ("chunks", ctypes.c_int64),
+        ("chunk", ctypes.c_int64),
     ]
 
 
@@ -108,6 +179,27 @@ _SIGNATURES = {
                                          ctypes.c_int32, ctypes.c_void_p]),
     "mx_dequantize": (ctypes.c_int, [ctypes.POINTER(QTensorDesc), ctypes.c_void_p,
                                      ctypes.c_int64, ctypes.c_void_p]),
+    "mx_rmsnorm_quantize": (ctypes.c_int, [ctypes.POINTER(NormDesc), ctypes.c_int32,
+                                           ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                           ctypes.c_uint64, ctypes.c_uint64, ctypes.c_void_p,
+                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.POINTER(QTensorDesc),
+                                           ctypes.POINTER(QTensorDesc), ctypes.c_void_p]),
+    "mx_rmsnorm_backward_workspace": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64,
+                                                     ctypes.POINTER(ctypes.c_size_t)]),
+    "mx_rmsnorm_backward": (ctypes.c_int, [ctypes.POINTER(NormGradDesc), ctypes.c_void_p,
+                                           ctypes.c_size_t, ctypes.c_void_p]),
+    "mx_grad_set_size": (ctypes.c_int, [ctypes.c_int32, ctypes.POINTER(GradDesc),
+                                        ctypes.POINTER(ctypes.c_size_t)]),
+    "mx_grad_set_fill": (ctypes.c_int, [ctypes.c_int32, ctypes.POINTER(GradDesc),
+                                        ctypes.c_void_p, ctypes.c_size_t,
+                                        ctypes.POINTER(GradSetDesc)]),
+    "mx_grad_workspace": (ctypes.c_size_t, []),
+    "mx_grad_norm": (ctypes.c_int, [ctypes.POINTER(GradSetDesc), ctypes.c_void_p,
+                                    ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "mx_grad_clip": (ctypes.c_int, [ctypes.POINTER(GradSetDesc), ctypes.POINTER(GradSetDesc),
+                                    ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
+                                    ctypes.c_size_t, ctypes.c_void_p]),
     "mx_status_string": (ctypes.c_char_p, [ctypes.c_int32]),
     "mx_version": (ctypes.c_char_p, []),
     "mx_last_hip_error": (ctypes.c_char_p, []),
@@ -413,3 +505,261 @@ def dequantize(q: QTensor, out=None, stream=None):
                            _stream_handle(q.codes.device, stream))
     _check(st, "mx_dequantize")
     return out
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _place(device, stream):
+    """(context, stream handle) of a call on `device`: inside the context the
+    device is current and torch allocates for the stream that the call runs on,
+    so that neither an output nor a workspace is memory another stream may
+    still be using."""
+    import torch
+    if stream is None:
+        handle = torch.cuda.current_stream(device).cuda_stream
+        here = device.index == torch.cuda.current_device()
+        return (_HERE if here else torch.cuda.device(device)), handle
+    if not hasattr(stream, "cuda_stream"):
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                  else torch.cuda.default_stream(device))
+    if stream.device != device:
+        raise ValueError("stream is on another device than the tensors")
+    return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def _row_dtype(t, name: str) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return OUT_DTYPES["bf16"]
+    if t.dtype == torch.float32:
+        return OUT_DTYPES["f32"]
+    raise ValueError(f"{name} must be bfloat16 or float32")
+
+
+def _rows_of(t, name: str, like=None) -> Tuple[Optional[int], int]:
+    """(address, leading dimension) of a 2-D CUDA matrix with unit column
+    stride, of like's type, shape and device."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA (HIP) tensor; there is no CPU path")
+    if like is not None and (t.dtype != like.dtype or t.shape != like.shape
+                             or t.device != like.device):
+        raise ValueError(f"{name} must have the type, shape and device of the other rows")
+    rows, cols = t.shape
+    if rows == 0 or cols == 0:
+        return None, (cols + 7) // 8 * 8
+    if t.stride(1) != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return t.data_ptr(), t.stride(0) if rows > 1 else (cols + 7) // 8 * 8
+
+
+def _vector(t, name: str, n: int, device):
+    if t.dim() != 1 or t.shape[0] != n or t.device != device:
+        raise ValueError(f"{name} must be a 1-D tensor of {n} elements on the rows' device")
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr() if n else None
+
+
+class RMSNormQuantized(NamedTuple):
+    """What rmsnorm_quantize returns: the axis-1 and axis-0 operands of y (q0 is
+    None without dual), the residual stream h and rstd per row."""
+    q1: QTensor
+    q0: Optional[QTensor]
+    h: object
+    rstd: object
+
+
+def rmsnorm_quantize(x, weight, residual=None, eps: float = 1e-5, format: str = "fp4_e2m1",
+                     dual: bool = False, rotate: str = "hadamard", round: str = "rne",
+                     seed1: int = 0, seed0: int = 0, h=None, stream=None) -> RMSNormQuantized:
+    """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight, and y rotated
+    and quantized into the operands the linears read (see mx_rmsnorm_quantize).
+
+    x, residual: 2-D bf16 or fp32 CUDA tensors (row-strided views allowed);
+    weight: bf16 or fp32 [cols]. format, rotate, round and the seeds are those
+    of quantize_dual / quantize_fp8; dual adds the axis-0 operand. h: where the
+    stream is written, may be residual or x itself to update it in place; x is
+    returned as h where there is no residual.
+    """
+    import torch
+    lib = load_library()
+    n = NormDesc()
+    n.x, n.ldx = _rows_of(x, "x")
+    n.dtype = _row_dtype(x, "x")
+    rows, cols = x.shape
+    n.rows, n.cols, n.eps = rows, cols, eps
+    n.weight = _vector(weight, "weight", cols, x.device)
+    n.weight_dtype = _row_dtype(weight, "weight")
+    sizes = quantize_fp8_sizes if FORMATS[format] else quantize_sizes
+    size1 = sizes(rows, cols, 1)
+    size0 = sizes(rows, cols, 0) if dual else (0, 0)
+    place, handle = _place(x.device, stream)
+    with place:
+        if residual is not None:
+            n.residual, n.ldr = _rows_of(residual, "residual", x)
+            if h is None:
+                h = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+            n.h, n.ldh = _rows_of(h, "h", x)
+        else:
+            if h is not None and h is not x:
+                raise ValueError("without a residual h is x itself")
+            h = x
+        rstd = torch.empty((rows,), dtype=torch.float32, device=x.device)
+        n.rstd = rstd.data_ptr() if rows else None
+        buf = [torch.empty((b,), dtype=torch.uint8, device=x.device)
+               for b in (size1 + size0 if dual else size1)]
+        ptr = [b.data_ptr() if b.numel() else None for b in buf]
+        d1, d0 = QTensorDesc(), QTensorDesc()
+        st = lib.mx_rmsnorm_quantize(ctypes.byref(n), FORMATS[format], 32, ROTATE[rotate],
+                                     ROUND[round], seed1 & 0xFFFFFFFFFFFFFFFF,
+                                     seed0 & 0xFFFFFFFFFFFFFFFF, ptr[0], ptr[1],
+                                     ptr[2] if dual else None, ptr[3] if dual else None,
+                                     ctypes.byref(d1), ctypes.byref(d0), handle)
+    _check(st, "mx_rmsnorm_quantize")
+    if not dual:
+        return RMSNormQuantized(QTensor(buf[0], buf[1], d1), None, h, rstd)
+    if not (rows and cols):     # empty operands have no buffers to tell the call by
+        d0 = QTensorDesc(None, None, rows, cols, 0, 32, ROTATE[rotate], ROUND[round],
+                         seed0 & 0xFFFFFFFFFFFFFFFF, FORMATS[format])
+    return RMSNormQuantized(QTensor(buf[0], buf[1], d1), QTensor(buf[2], buf[3], d0), h, rstd)
+
+
+def rmsnorm_backward(dy, h, rstd, weight, dres=None, dh=None, stream=None):
+    """Gradient of rmsnorm_quantize (see mx_rmsnorm_backward): returns (dh,
+    dweight). dy: gradient of y; h, rstd: what the forward call returned; dres:
+    the gradient that reaches h past the norm. dh is the gradient of x and of
+    residual; it may be written over dy or dres. dweight is fp32."""
+    import torch
+    lib = load_library()
+    g = NormGradDesc()
+    g.dy, g.lddy = _rows_of(dy, "dy")
+    g.dtype = _row_dtype(dy, "dy")
+    rows, cols = dy.shape
+    g.rows, g.cols = rows, cols
+    g.h, g.ldh = _rows_of(h, "h", dy)
+    if dres is not None:
+        g.dres, g.ldres = _rows_of(dres, "dres", dy)
+    if rstd.dtype != torch.float32:
+        raise ValueError("rstd must be float32")
+    g.rstd = _vector(rstd, "rstd", rows, dy.device)
+    g.weight = _vector(weight, "weight", cols, dy.device)
+    g.weight_dtype = _row_dtype(weight, "weight")
+    need = ctypes.c_size_t()
+    _check(lib.mx_rmsnorm_backward_workspace(rows, cols, ctypes.byref(need)),
+           "mx_rmsnorm_backward_workspace")
+    place, handle = _place(dy.device, stream)
+    with place:
+        if dh is None:
+            dh = torch.empty((rows, cols), dtype=dy.dtype, device=dy.device)
+        g.dh, g.lddh = _rows_of(dh, "dh", dy)
+        dweight = torch.empty((cols,), dtype=torch.float32, device=dy.device)
+        g.dweight = dweight.data_ptr() if cols else None
+        work = torch.empty((need.value,), dtype=torch.uint8, device=dy.device)
+        st = lib.mx_rmsnorm_backward(ctypes.byref(g), work.data_ptr() if need.value else None,
+                                     need.value, handle)
+    _check(st, "mx_rmsnorm_backward")
+    return dh, dweight
+
+
+class GradSet:
+    """Gradient tensors laid out once for grad_norm and clip_grad_norm (see
+    mx_grad_set): fp32 and bf16 CUDA tensors of one device, mixed as they come,
+    contiguous or (1-D and 2-D) row-strided. It holds the tensors and their
+    addresses: make another when one is replaced. It cannot be made while a
+    graph is captured (its table is copied to the device)."""
+
+    def __init__(self, tensors):
+        import torch
+        lib = load_library()
+        self.tensors = list(tensors)
+        self.device = self.tensors[0].device if self.tensors else None
+        self._grads = (GradDesc * max(1, len(self.tensors)))()
+        for g, t in zip(self._grads, self.tensors):
+            if not t.is_cuda or t.device != self.device:
+                raise ValueError("gradients must be CUDA (HIP) tensors of one device")
+            g.dtype = _row_dtype(t, "a gradient")
+            g.data = t.data_ptr() if t.numel() else None
+            if t.dim() == 1:
+                g.rows, g.cols, g.ld = t.shape[0], 1, t.stride(0)
+            elif t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1):
+                g.rows, g.cols, g.ld = t.shape[0], t.shape[1], t.stride(0)
+            elif t.is_contiguous():
+                g.rows, g.cols, g.ld = 1, t.numel(), t.numel()
+            else:
+                raise ValueError("a gradient must be contiguous or a row-strided matrix")
+        need = ctypes.c_size_t()
+        _check(lib.mx_grad_set_size(len(self.tensors), self._grads, ctypes.byref(need)),
+               "mx_grad_set_size")
+        self._host = torch.zeros((need.value,), dtype=torch.uint8)
+        self.desc = GradSetDesc()
+        _check(lib.mx_grad_set_fill(len(self.tensors), self._grads,
+                                    self._host.data_ptr() if need.value else None, need.value,
+                                    ctypes.byref(self.desc)), "mx_grad_set_fill")
+        if need.value:
+            self._table = self._host.to(self.device)
+            self.desc.table = self._table.data_ptr()
+
+
+def _grads_and_device(grads):
+    """A GradSet or a list of tensors as it is, and the device it is on."""
+    import torch
+    if not isinstance(grads, GradSet):
+        grads = list(grads)
+        device = grads[0].device if grads else None
+    else:
+        device = grads.device
+    if device is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    elif device.type != "cuda":
+        raise ValueError("gradients must be CUDA (HIP) tensors; there is no CPU path")
+    return grads, device
+
+
+def _as_set(grads) -> GradSet:
+    return grads if isinstance(grads, GradSet) else GradSet(grads)
+
+
+def _norm_buffers(device, lib):
+    import torch
+    size = lib.mx_grad_workspace()
+    return (torch.empty((), dtype=torch.float32, device=device),
+            torch.empty((size,), dtype=torch.uint8, device=device), size)
+
+
+def grad_norm(grads, stream=None):
+    """Global 2-norm of a GradSet or of a list of gradients (see mx_grad_norm),
+    a 0-dimensional fp32 CUDA tensor; with a GradSet nothing waits for the GPU."""
+    lib = load_library()
+    grads, device = _grads_and_device(grads)
+    place, handle = _place(device, stream)
+    with place:
+        s = _as_set(grads)
+        norm, work, size = _norm_buffers(device, lib)
+        st = lib.mx_grad_norm(ctypes.byref(s.desc), norm.data_ptr(), work.data_ptr(), size, handle)
+    _check(st, "mx_grad_norm")
+    return norm
+
+
+def clip_grad_norm(grads, max_norm: float, out=None, stream=None):
+    """Scale gradients by min(1, max_norm / (norm + 1e-6)), norm their global
+    2-norm, which is returned as grad_norm returns it (see mx_grad_clip). In
+    place, or into `out`: tensors of the same shapes and types. Both may be
+    GradSets, made once, or lists."""
+    lib = load_library()
+    grads, device = _grads_and_device(grads)
+    if out is not None:
+        out, there = _grads_and_device(out)
+        if there != device:
+            raise ValueError("out must be on the gradients' device")
+    place, handle = _place(device, stream)
+    with place:
+        s = _as_set(grads)
+        o = s if out is None else _as_set(out)
+        norm, work, size = _norm_buffers(device, lib)
+        st = lib.mx_grad_clip(ctypes.byref(s.desc), ctypes.byref(o.desc), max_norm,
+                              norm.data_ptr(), work.data_ptr(), size, handle)
+    _check(st, "mx_grad_clip")
+    return norm

@@ -1,9 +1,12 @@
-// C ABI of the MXFP4 library (and its MXFP8 comparator): argument validation
-// and launch dispatch.
+// C ABI of the MXFP4 library (its MXFP8 comparator, the norm and the gradient
+// clipping included): argument validation and launch dispatch.
 // Every check runs on the host before anything is enqueued, so an invalid
 // call launches nothing and writes nothing.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
 
 #include "../../include/mxfp4.h"
 #include "mx_kernels.h"
@@ -393,6 +396,356 @@ mx_status mx_dequantize(const mx_qtensor *q, float *out, int64_t ld, void *strea
   a.out = out;
   a.ld = ld;
   return hip_status(mx::dequantize_launch(a, static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+
+bool valid_dtype(int32_t t) { return t == MX_OUT_F32 || t == MX_OUT_BF16; }
+int64_t dtype_size(int32_t t) { return t == MX_OUT_F32 ? 4 : 2; }
+
+// A [rows, cols] matrix that the norm kernels read or write in 16-byte units.
+mx_status check_rows(const void *p, int64_t rows, int64_t cols, int64_t ld, int32_t dtype) {
+  if (p == nullptr) return MX_ERR_NULL;
+  if (ld < cols) return MX_ERR_SHAPE;
+  if (!aligned(p, 16) || ld % (16 / dtype_size(dtype)) != 0) return MX_ERR_ALIGN;
+  if (span_too_large(rows, ld, dtype_size(dtype))) return MX_ERR_UNSUPPORTED;
+  return MX_OK;
+}
+
+}  // namespace
+
+mx_status mx_rmsnorm_quantize(const mx_norm *n, int32_t format, int32_t block, int32_t rotate,
+                              int32_t round, uint64_t seed1, uint64_t seed0, void *codes1,
+                              void *scales1, void *codes0, void *scales0, mx_qtensor *desc1,
+                              mx_qtensor *desc0, void *stream) {
+  if (n == nullptr) return MX_ERR_NULL;
+  if (block != 32) return MX_ERR_ARG;
+  if (!valid_rotate(rotate) || !valid_round(round) || !valid_format(format)) return MX_ERR_ARG;
+  if (format == MX_FMT_FP8_E4M3 && round != MX_ROUND_RNE) return MX_ERR_ARG;
+  if (!valid_dtype(n->dtype) || !valid_dtype(n->weight_dtype)) return MX_ERR_ARG;
+  if (!(n->eps >= 0.0) || std::isinf(n->eps)) return MX_ERR_ARG;
+  const int64_t rows = n->rows, cols = n->cols;
+  if (rows < 0 || cols < 0) return MX_ERR_SHAPE;
+  const bool dual = codes0 != nullptr || scales0 != nullptr;
+  if (cols % 32 != 0 || (dual && rows % 32 != 0)) return MX_ERR_SHAPE;
+  const bool empty = rows == 0 || cols == 0;
+  if (!empty) {
+    if (n->weight == nullptr || n->rstd == nullptr || codes1 == nullptr || scales1 == nullptr ||
+        (dual && (codes0 == nullptr || scales0 == nullptr)))
+      return MX_ERR_NULL;
+    if (extents_too_large(rows, cols)) return MX_ERR_UNSUPPORTED;
+    mx_status st = check_rows(n->x, rows, cols, n->ldx, n->dtype);
+    if (st != MX_OK) return st;
+    if (n->residual != nullptr) {
+      st = check_rows(n->residual, rows, cols, n->ldr, n->dtype);
+      if (st != MX_OK) return st;
+      st = check_rows(n->h, rows, cols, n->ldh, n->dtype);
+      if (st != MX_OK) return st;
+      if ((n->h == n->x && n->ldh != n->ldx) || (n->h == n->residual && n->ldh != n->ldr))
+        return MX_ERR_SHAPE;
+    }
+    if (!aligned(n->weight, 16) || !aligned(n->rstd, 4) || !aligned(codes1, 16) ||
+        !aligned(scales1, 4) || (dual && (!aligned(codes0, 16) || !aligned(scales0, 4))))
+      return MX_ERR_ALIGN;
+    for (int axis = dual ? 0 : 1; axis < 2; ++axis) {
+      int64_t mnp, kp;
+      padded_extents(rows, cols, axis, &mnp, &kp);
+      if (mnp * kp * code_bytes_x2(format) / 2 >= kMaxCodeBytes) return MX_ERR_UNSUPPORTED;
+    }
+  }
+  fill_desc(desc1, codes1, scales1, rows, cols, 1, block, rotate, round, seed1, format);
+  if (dual) fill_desc(desc0, codes0, scales0, rows, cols, 0, block, rotate, round, seed0, format);
+  if (empty) return MX_OK;
+
+  mx::NormArgs a;
+  a.x = n->x;
+  a.residual = n->residual;
+  a.weight = n->weight;
+  a.h = n->residual != nullptr ? n->h : const_cast<void *>(n->x);   // never written without one
+  a.rstd = n->rstd;
+  a.rows = rows;
+  a.cols = cols;
+  a.ldx = n->ldx;
+  a.ldr = n->ldr;
+  a.ldh = n->residual != nullptr ? n->ldh : n->ldx;
+  a.f32 = n->dtype == MX_OUT_F32 ? 1 : 0;
+  a.wf32 = n->weight_dtype == MX_OUT_F32 ? 1 : 0;
+  a.eps = n->eps;
+  a.rotate = rotate;
+  a.round = round;
+  a.fmt = format == MX_FMT_FP8_E4M3 ? 1 : 0;
+  a.seed1_lo = (uint32_t)(seed1 & 0xFFFFFFFFull);
+  a.seed1_hi = (uint32_t)(seed1 >> 32);
+  a.seed0_lo = (uint32_t)(seed0 & 0xFFFFFFFFull);
+  a.seed0_hi = (uint32_t)(seed0 >> 32);
+  a.codes1 = static_cast<uint8_t *>(codes1);
+  a.scales1 = static_cast<uint8_t *>(scales1);
+  a.codes0 = static_cast<uint8_t *>(codes0);
+  a.scales0 = static_cast<uint8_t *>(scales0);
+  return hip_status(mx::norm_launch(a, static_cast<hipStream_t>(stream)));
+}
+
+mx_status mx_rmsnorm_backward_workspace(int64_t rows, int64_t cols, size_t *bytes) {
+  if (bytes == nullptr) return MX_ERR_NULL;
+  if (rows < 0 || cols < 0) return MX_ERR_SHAPE;
+  if (extents_too_large(rows, cols)) return MX_ERR_UNSUPPORTED;
+  *bytes = (size_t)mx::norm_grad_groups(rows) * (size_t)cols * sizeof(float);
+  return MX_OK;
+}
+
+mx_status mx_rmsnorm_backward(const mx_norm_grad *g, void *workspace, size_t workspace_bytes,
+                              void *stream) {
+  if (g == nullptr) return MX_ERR_NULL;
+  if (!valid_dtype(g->dtype) || !valid_dtype(g->weight_dtype)) return MX_ERR_ARG;
+  const int64_t rows = g->rows, cols = g->cols;
+  size_t need = 0;
+  mx_status st = mx_rmsnorm_backward_workspace(rows, cols, &need);
+  if (st != MX_OK) return st;
+  if (cols % 8 != 0) return MX_ERR_SHAPE;
+  if (cols == 0) return MX_OK;
+  if (g->dweight == nullptr) return MX_ERR_NULL;
+  if (!aligned(g->dweight, 16)) return MX_ERR_ALIGN;
+  if (rows > 0) {
+    if (g->rstd == nullptr || g->weight == nullptr || workspace == nullptr) return MX_ERR_NULL;
+    const void *m[4] = {g->dy, g->h, g->dh, g->dres};
+    const int64_t ld[4] = {g->lddy, g->ldh, g->lddh, g->ldres};
+    for (int i = 0; i < (g->dres != nullptr ? 4 : 3); ++i) {
+      st = check_rows(m[i], rows, cols, ld[i], g->dtype);
+      if (st != MX_OK) return st;
+    }
+    if ((g->dh == g->dy && g->lddh != g->lddy) || (g->dh == g->dres && g->lddh != g->ldres) ||
+        workspace_bytes < need)
+      return MX_ERR_SHAPE;
+    if (!aligned(g->rstd, 4) || !aligned(g->weight, 16) || !aligned(workspace, 16))
+      return MX_ERR_ALIGN;
+  }
+  mx::NormGradArgs a;
+  a.dy = g->dy;
+  a.h = g->h;
+  a.dres = g->dres;
+  a.rstd = g->rstd;
+  a.weight = g->weight;
+  a.dh = g->dh;
+  a.dweight = g->dweight;
+  a.partial = static_cast<float *>(workspace);
+  a.rows = rows;
+  a.cols = cols;
+  a.lddy = g->lddy;
+  a.ldh = g->ldh;
+  a.ldres = g->ldres;
+  a.lddh = g->lddh;
+  a.f32 = g->dtype == MX_OUT_F32 ? 1 : 0;
+  a.wf32 = g->weight_dtype == MX_OUT_F32 ? 1 : 0;
+  return hip_status(mx::norm_grad_launch(a, static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+
+// A set's table: the tensors, the chunks, then the indices of the tensors
+// without gaps by address (host only, for the overlap checks).
+struct GradLayout {
+  int64_t chunks, chunk, ordered;
+  size_t chunks_at, order_at, bytes;
+};
+
+bool grad_empty(const mx_grad &g) { return g.rows == 0 || g.cols == 0; }
+bool grad_gapless(const mx_grad &g) { return g.rows <= 1 || g.ld == g.cols; }
+int64_t grad_bytes(const mx_grad &g) { return g.rows * g.cols * dtype_size(g.dtype); }
+
+mx_status grad_layout(int32_t count, const mx_grad *grads, GradLayout *l) {
+  if (count < 0) return MX_ERR_ARG;
+  if (count > 0 && grads == nullptr) return MX_ERR_NULL;
+  int64_t total = 0;
+  l->ordered = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    const mx_grad &g = grads[i];
+    if (!valid_dtype(g.dtype)) return MX_ERR_ARG;
+    if (g.rows < 0 || g.cols < 0) return MX_ERR_SHAPE;
+    if (grad_empty(g)) continue;
+    if (g.data == nullptr) return MX_ERR_NULL;
+    if (g.rows > 1 && g.ld < g.cols) return MX_ERR_SHAPE;
+    if (!aligned(g.data, (uintptr_t)dtype_size(g.dtype))) return MX_ERR_ALIGN;
+    // spans and the total stay below 2^62 bytes
+    const int64_t pitch = g.rows > 1 ? g.ld : g.cols;
+    if (pitch > (((int64_t)1 << 62) / dtype_size(g.dtype)) / g.rows) return MX_ERR_UNSUPPORTED;
+    total += g.rows * g.cols;
+    if (total > ((int64_t)1 << 60)) return MX_ERR_UNSUPPORTED;
+    if (grad_gapless(g)) ++l->ordered;
+  }
+  // Elements per chunk: enough chunks for every workgroup to walk several
+  // (the last round of them idles little), none so small that looking it up
+  // shows, none so large that one tensor's last chunk does.
+  l->chunk = 2048;
+  while (l->chunk < 32768 && total / l->chunk > 16 * mx::kGradGroups) l->chunk *= 2;
+  l->chunks = 0;
+  for (int32_t i = 0; i < count; ++i)
+    l->chunks += (grads[i].rows * grads[i].cols + l->chunk - 1) / l->chunk;
+  if (l->chunks > ((int64_t)1 << 31)) return MX_ERR_UNSUPPORTED;
+  l->chunks_at = (size_t)count * sizeof(mx::GradTensor);
+  l->order_at = l->chunks_at + (size_t)l->chunks * sizeof(mx::GradChunk);
+  l->bytes = l->order_at + (size_t)((l->ordered + 1) / 2 * 2) * sizeof(uint32_t);
+  return MX_OK;
+}
+
+mx_status check_set(const mx_grad_set *s) {
+  if (s == nullptr) return MX_ERR_NULL;
+  if (s->count < 0 || s->chunks < 0) return MX_ERR_ARG;
+  if (s->chunks > 0) {
+    if (s->grads == nullptr || s->host_table == nullptr || s->table == nullptr) return MX_ERR_NULL;
+    if (!aligned(s->table, 8)) return MX_ERR_ALIGN;
+  }
+  return MX_OK;
+}
+
+mx_status check_norm_outputs(const float *norm, const void *workspace, size_t workspace_bytes) {
+  if (norm == nullptr || workspace == nullptr) return MX_ERR_NULL;
+  if (workspace_bytes < mx_grad_workspace()) return MX_ERR_SHAPE;
+  if (!aligned(norm, 4) || !aligned(workspace, 8)) return MX_ERR_ALIGN;
+  return MX_OK;
+}
+
+mx::GradTable grad_table(const mx_grad_set *s) {
+  mx::GradTable t;
+  t.tensors = static_cast<const mx::GradTensor *>(s->table);
+  t.chunk_of = reinterpret_cast<const mx::GradChunk *>(static_cast<const uint8_t *>(s->table) +
+                                                       (size_t)s->count * sizeof(mx::GradTensor));
+  t.chunks = s->chunks;
+  t.chunk = s->chunk;
+  return t;
+}
+
+// The tensors without gaps of a filled set, by address.
+const uint32_t *grad_order(const mx_grad_set *s, int64_t *n) {
+  const size_t at = (size_t)s->count * sizeof(mx::GradTensor) +
+                    (size_t)s->chunks * sizeof(mx::GradChunk);
+  *n = 0;
+  for (int32_t i = 0; i < s->count; ++i)
+    *n += !grad_empty(s->grads[i]) && grad_gapless(s->grads[i]);
+  return reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(s->host_table) + at);
+}
+
+uintptr_t address(const mx_grad &g) { return reinterpret_cast<uintptr_t>(g.data); }
+
+// Whether tensors of two sets share memory other than place by place: both
+// sets' tensors without gaps, merged by address.
+bool grad_sets_clash(const mx_grad_set *a, const mx_grad_set *b) {
+  int64_t na, nb;
+  const uint32_t *oa = grad_order(a, &na), *ob = grad_order(b, &nb);
+  for (int64_t i = 0, j = 0; i < na && j < nb;) {
+    const mx_grad &p = a->grads[oa[i]], &q = b->grads[ob[j]];
+    const uintptr_t pe = address(p) + (uintptr_t)grad_bytes(p);
+    const uintptr_t qe = address(q) + (uintptr_t)grad_bytes(q);
+    if (pe <= address(q)) {
+      ++i;
+    } else if (qe <= address(p)) {
+      ++j;
+    } else {
+      if (oa[i] != ob[j] || p.data != q.data) return true;
+      ++i;
+      ++j;
+    }
+  }
+  return false;
+}
+
+}  // namespace
+
+mx_status mx_grad_set_size(int32_t count, const mx_grad *grads, size_t *table_bytes) {
+  if (table_bytes == nullptr) return MX_ERR_NULL;
+  GradLayout l;
+  const mx_status st = grad_layout(count, grads, &l);
+  if (st != MX_OK) return st;
+  *table_bytes = l.bytes;
+  return MX_OK;
+}
+
+mx_status mx_grad_set_fill(int32_t count, const mx_grad *grads, void *host_table,
+                           size_t table_bytes, mx_grad_set *set) {
+  if (set == nullptr) return MX_ERR_NULL;
+  GradLayout l;
+  const mx_status st = grad_layout(count, grads, &l);
+  if (st != MX_OK) return st;
+  if (l.bytes > 0 && host_table == nullptr) return MX_ERR_NULL;
+  if (table_bytes < l.bytes) return MX_ERR_SHAPE;
+  if (!aligned(host_table, 8)) return MX_ERR_ALIGN;
+  uint8_t *base = static_cast<uint8_t *>(host_table);
+  // Tensors with gaps only clash here when the same one is given twice (column
+  // slices of one buffer do not): sort them in the order's place, look, then
+  // sort the others.
+  uint32_t *order = reinterpret_cast<uint32_t *>(base + l.order_at);
+  auto by_address = [&](uint32_t i, uint32_t j) { return address(grads[i]) < address(grads[j]); };
+  int64_t n = 0;
+  for (int32_t i = 0; i < count; ++i)
+    if (!grad_empty(grads[i]) && grad_gapless(grads[i])) order[n++] = (uint32_t)i;
+  std::sort(order, order + n, by_address);
+  for (int64_t i = 1; i < n; ++i)
+    if (address(grads[order[i - 1]]) + (uintptr_t)grad_bytes(grads[order[i - 1]]) >
+        address(grads[order[i]]))
+      return MX_ERR_ARG;
+  mx::GradTensor *t = reinterpret_cast<mx::GradTensor *>(base);
+  // the tensors' place holds the ones with gaps while they are compared
+  uint32_t *gaps = reinterpret_cast<uint32_t *>(t);
+  int64_t m = 0;
+  for (int32_t i = 0; i < count; ++i)
+    if (!grad_empty(grads[i]) && !grad_gapless(grads[i])) gaps[m++] = (uint32_t)i;
+  std::sort(gaps, gaps + m, by_address);
+  for (int64_t i = 1; i < m; ++i)
+    if (address(grads[gaps[i - 1]]) == address(grads[gaps[i]])) return MX_ERR_ARG;
+  mx::GradChunk *c = reinterpret_cast<mx::GradChunk *>(base + l.chunks_at);
+  for (int32_t i = 0; i < count; ++i) {
+    const mx_grad &g = grads[i];
+    t[i].data = g.data;
+    t[i].rows = g.rows;
+    t[i].cols = g.cols;
+    t[i].ld = grad_gapless(g) ? g.cols : g.ld;
+    t[i].f32 = g.dtype == MX_OUT_F32 ? 1 : 0;
+    const int64_t k = (g.rows * g.cols + l.chunk - 1) / l.chunk;
+    for (int64_t j = 0; j < k; ++j) *c++ = mx::GradChunk{(uint32_t)i, (uint32_t)j};
+  }
+  set->grads = grads;
+  set->count = count;
+  set->host_table = host_table;
+  set->table = nullptr;
+  set->table_bytes = l.bytes;
+  set->chunks = l.chunks;
+  set->chunk = l.chunk;
+  return MX_OK;
+}
+
+size_t mx_grad_workspace(void) { return mx::kGradGroups * sizeof(double); }
+
+mx_status mx_grad_norm(const mx_grad_set *set, float *norm, void *workspace,
+                       size_t workspace_bytes, void *stream) {
+  mx_status st = check_set(set);
+  if (st != MX_OK) return st;
+  st = check_norm_outputs(norm, workspace, workspace_bytes);
+  if (st != MX_OK) return st;
+  return hip_status(mx::grad_norm_launch(grad_table(set), static_cast<double *>(workspace), norm,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+mx_status mx_grad_clip(const mx_grad_set *in, const mx_grad_set *out, float max_norm, float *norm,
+                       void *workspace, size_t workspace_bytes, void *stream) {
+  mx_status st = check_set(in);
+  if (st != MX_OK) return st;
+  if (out == nullptr) out = in;
+  st = check_set(out);
+  if (st != MX_OK) return st;
+  if (!(max_norm >= 0.0f)) return MX_ERR_ARG;
+  st = check_norm_outputs(norm, workspace, workspace_bytes);
+  if (st != MX_OK) return st;
+  if (out != in) {
+    if (out->count != in->count || out->chunks != in->chunks || out->chunk != in->chunk)
+      return MX_ERR_MISMATCH;
+    for (int32_t i = 0; i < in->count; ++i) {
+      const mx_grad &p = in->grads[i], &q = out->grads[i];
+      if (p.rows != q.rows || p.cols != q.cols || p.dtype != q.dtype) return MX_ERR_MISMATCH;
+    }
+    if (grad_sets_clash(in, out)) return MX_ERR_ARG;
+  }
+  return hip_status(mx::grad_clip_launch(grad_table(in), grad_table(out),
+                                         static_cast<double *>(workspace), max_norm, norm,
+                                         static_cast<hipStream_t>(stream)));
 }
 
 const char *mx_status_string(int32_t status) {

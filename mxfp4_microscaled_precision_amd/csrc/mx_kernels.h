@@ -106,4 +106,62 @@ struct DequantArgs {
 
 hipError_t dequantize_launch(const DequantArgs &a, hipStream_t stream);
 
+// RMS norm into the axis-1 operand and, unless codes0 is null, the axis-0 one
+// (rows % 32 == 0).
+struct NormArgs {
+  const void *x, *residual;        // [rows, cols] bf16 or fp32; residual may be null
+  const void *weight;              // [cols] bf16 or fp32
+  void *h;                         // x + residual (x itself without a residual)
+  float *rstd;                     // [rows]
+  int64_t rows, cols, ldx, ldr, ldh;
+  int f32, wf32;                   // rows / weight are fp32
+  double eps;
+  int rotate, round, fmt;
+  uint32_t seed1_lo, seed1_hi;     // axis-1 operand
+  uint32_t seed0_lo, seed0_hi;     // axis-0 operand
+  uint8_t *codes1, *scales1;
+  uint8_t *codes0, *scales0;
+};
+
+hipError_t norm_launch(const NormArgs &a, hipStream_t stream);
+
+// Gradient of the norm.
+struct NormGradArgs {
+  const void *dy, *h, *dres;       // [rows, cols] bf16 or fp32; dres may be null
+  const float *rstd;               // [rows]
+  const void *weight;              // [cols]
+  void *dh;                        // [rows, cols]
+  float *dweight;                  // [cols]
+  float *partial;                  // [norm_grad_groups(rows)][cols]
+  int64_t rows, cols, lddy, ldh, ldres, lddh;
+  int f32, wf32;
+};
+
+// Workgroups of the gradient's row pass, one partial weight gradient each. A
+// function of the shape alone, so that the order of the sums is too.
+inline int norm_grad_groups(int64_t rows) { return (int)(rows < 512 ? rows : 512); }
+
+hipError_t norm_grad_launch(const NormGradArgs &a, hipStream_t stream);
+
+// Gradient tensors and their chunks, as a table in device memory.
+struct GradTensor {
+  void *data;
+  int64_t rows, cols, ld;          // ld == cols: no gaps
+  int64_t f32;                     // fp32, else bf16
+};
+struct GradChunk {
+  uint32_t tensor, at;             // elements [at * chunk, (at + 1) * chunk) of a tensor
+};
+struct GradTable {
+  const GradTensor *tensors;
+  const GradChunk *chunk_of;
+  int64_t chunks, chunk;
+};
+
+constexpr int kGradGroups = 2048;  // workgroups, and partial sums, at most
+
+hipError_t grad_norm_launch(const GradTable &t, double *partial, float *norm, hipStream_t stream);
+hipError_t grad_clip_launch(const GradTable &in, const GradTable &out, double *partial,
+                            float max_norm, float *norm, hipStream_t stream);
+
 }  // namespace mx

@@ -69,6 +69,7 @@ What pins each function (tests/test_oracle_*.py, all "not gpu"):
   round_e2m1_sr         unbiasedness over 10^4 seeds; limits f -> 0 and 1.
   quantize_ref          worked one-hot / constant / zero / NaN blocks;
                         re-quantizing a representable block is a fixed point.
+  quantize_values_ref   quantize_ref is it after widening.
   tile_codes/scales     element-by-element address formula written out in a
                         test loop; round trip through untile_*.
   operand_mse           exhaustive search for the nearest E2M1 value of every
@@ -109,6 +110,7 @@ __all__ = [
     "round_e2m1_sr",
     "QuantRef",
     "quantize_ref",
+    "quantize_values_ref",
     "dequantize_ref",
     "pack_codes",
     "unpack_codes",
@@ -427,16 +429,27 @@ def quantize_ref(x_bits: np.ndarray, axis: int, block: int = MX_BLOCK,
     (they set the random-sign index k and the stochastic-rounding index L).
     Along `axis` the slice must start at a multiple of 32 and be contiguous.
     """
+    # 1. widen bf16 -> fp32 (exact)
+    return quantize_values_ref(_bf16_to_f32(np.asarray(x_bits, dtype=np.uint16)), axis, block,
+                               rotate, rounding, seed, row_index=row_index, col_index=col_index,
+                               total_cols=total_cols, fmt=fmt)
+
+
+def quantize_values_ref(x: np.ndarray, axis: int, block: int = MX_BLOCK,
+                        rotate: str = ROT_HADAMARD, rounding: str = ROUND_RNE,
+                        seed: int = 0, *, row_index: Optional[np.ndarray] = None,
+                        col_index: Optional[np.ndarray] = None,
+                        total_cols: Optional[int] = None, fmt: str = FMT_FP4) -> QuantRef:
+    """quantize_ref of an fp32 tensor (its source widened, or the norm's y)."""
     if block != MX_BLOCK:
         raise ValueError("only 32-element blocks are defined")
-    x_bits = np.asarray(x_bits, dtype=np.uint16)
-    R, C = x_bits.shape
+    x = np.asarray(x, dtype=np.float32)
+    R, C = x.shape
     rows = np.arange(R, dtype=np.int64) if row_index is None else np.asarray(row_index, np.int64)
     cols = np.arange(C, dtype=np.int64) if col_index is None else np.asarray(col_index, np.int64)
     ncols = C if total_cols is None else int(total_cols)
 
-    # 1. widen bf16 -> fp32 (exact) and orient reduction-major: [MN, K]
-    x = _bf16_to_f32(x_bits)
+    # orient reduction-major: [MN, K]
     if axis == 1:
         xk = x
         k_index = cols
