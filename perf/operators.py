@@ -246,10 +246,15 @@ def _run_clip(s):
 
 
 def _own_operand(q, s):
-    if s["case"]["format"] == "fp4_e2m1":
-        codes = torch.index_select(s["pairs"], 0, q.codes.int())
-    else:
-        codes = q.codes
+    fp4 = s["case"]["format"] == "fp4_e2m1"
+    codes = torch.index_select(s["pairs"], 0, q.codes.int()) if fp4 else q.codes
+    if s["case"]["rotate"] == "hadamard16":
+        # _hadamard negates the second half of a block after its 16-point
+        # rotation, the package does not: the values come in _hadamard's signs
+        # (eight of them at a time: the sign bits of half the words)
+        words = codes.view(torch.int64)
+        half = words.view(-1, 4)[:, 2:] if fp4 else words.view(-1, 8, 32)[:, 1::2]
+        half.bitwise_xor_(-0x7F7F7F7F7F7F7F80)
     return codes.view(torch.float8_e4m3fn), q.scales.view(torch.float8_e8m0fnu)
 
 
