@@ -471,6 +471,7 @@ mx_status mx_rmsnorm_quantize(const mx_norm *n, int32_t format, int32_t block, i
   a.f32 = n->dtype == MX_OUT_F32 ? 1 : 0;
   a.wf32 = n->weight_dtype == MX_OUT_F32 ? 1 : 0;
   a.eps = n->eps;
+  a.inv_cols = 1.0 / (double)cols;
   a.rotate = rotate;
   a.round = round;
   a.fmt = format == MX_FMT_FP8_E4M3 ? 1 : 0;

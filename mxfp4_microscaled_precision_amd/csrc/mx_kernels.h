@@ -115,7 +115,7 @@ struct NormArgs {
   float *rstd;                     // [rows]
   int64_t rows, cols, ldx, ldr, ldh;
   int f32, wf32;                   // rows / weight are fp32
-  double eps;
+  double eps, inv_cols;            // inv_cols = 1 / cols
   int rotate, round, fmt;
   uint32_t seed1_lo, seed1_hi;     // axis-1 operand
   uint32_t seed0_lo, seed0_hi;     // axis-0 operand

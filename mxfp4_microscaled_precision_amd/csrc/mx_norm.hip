@@ -30,6 +30,7 @@ namespace mx {
 
 namespace {
 
+
 // The row's h from x and the residual: bf16 rows round the sum to bf16 (exact
 // in fp32 wherever that matters: fp32 holds two bf16 values less than 16
 // binades apart, and beyond that the smaller one is below half a step).
@@ -50,8 +51,19 @@ __device__ __forceinline__ double add_squares(double acc, const float (&v)[8]) {
   return acc;
 }
 
-__device__ __forceinline__ float rstd_of(double sum, int64_t cols, double eps) {
-  return (float)(1.0 / __builtin_sqrt(sum / (double)cols + eps));
+// 1 / sqrt(sum / n + eps) from the hardware's reciprocal root (some 26 bits)
+// and two Newton steps, which take it to about 2^-51: a division and a root of
+// full precision would be four times as many dependent instructions, on the
+// path of every workgroup. Zero, infinity and NaN are the hardware's result.
+__device__ __forceinline__ float rstd_of(double sum, double inv_n, double eps) {
+  const double t = __builtin_fma(sum, inv_n, eps);
+  double y = __builtin_amdgcn_rsq(t);
+  const double half = -0.5 * t;
+  if (t > 0.0 && t < __builtin_inf()) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) y = __builtin_fma(__builtin_fma(half * y, y, 0.5), y, y);
+  }
+  return (float)y;
 }
 
 // ---------------------------------------------------------------------------
@@ -76,17 +88,21 @@ __global__ __launch_bounds__(256) void norm_rows_kernel(NormArgs a) {
   __shared__ double part[4];
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = acc;
   __syncthreads();
-  if (threadIdx.x == 0) a.rstd[r] = rstd_of(part[0] + part[1] + part[2] + part[3], a.cols, a.eps);
+  if (threadIdx.x == 0) a.rstd[r] = rstd_of(part[0] + part[1] + part[2] + part[3], a.inv_cols, a.eps);
 }
 
 // ---------------------------------------------------------------------------
-// A tile of y (16 rows x 128 columns, fp32) in LDS: the 16-byte chunk c of row
-// r lies at r * 512 + (c ^ r) * 16, so that 16 lanes that read one chunk of 16
-// rows, or write 16 chunks of one row, touch distinct banks.
+// The axis-1 operand in one pass: a workgroup takes 4 rows, a wave units of 4
+// rows x 512 columns (64 blocks, one per lane). Wave w of W holds unit w of h
+// in registers, as the rows' type, while the sums of squares meet in LDS; the
+// units from W on (rows wider than W of them) are read again, from cache, by
+// the lanes that wrote them. Each unit's y then goes through LDS as fp32, from
+// the lanes that loaded it (8 columns of each row) to those that encode it
+// (lane l: row l % 4, block l / 4).
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float *tile_chunk(float *st, int r, int c) {
-  return st + r * 128 + ((c ^ r) << 2);
-}
+constexpr int kRows = 4;
+constexpr int kUnitCols = 512;
+constexpr int kUnitBlocks = kUnitCols / 32;
 
 __device__ __forceinline__ void wave_lds_sync() {
   __builtin_amdgcn_wave_barrier();
@@ -94,99 +110,201 @@ __device__ __forceinline__ void wave_lds_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Encode the tile (row group g, K slice q) of the axis-1 operand whose y the
-// wave has put into st: lane l takes row l % 16, block l / 16.
-template <int ROT, int RND, int FMT>
-__device__ __forceinline__ void encode_tile(const NormArgs &a, float *st, uint32_t *sg, uint32_t g,
-                                            uint32_t q, uint32_t nslices, int64_t mnp) {
-  const int lane = threadIdx.x & 63;
-  const int rr = lane & 15, cb = lane >> 4;
-  const int64_t r = (int64_t)g * 16 + rr;
-  const int64_t kb = (int64_t)q * 4 + cb;
-  const bool valid = r < a.rows && (kb << 5) < a.cols;
-  float y[32];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float4 f = *reinterpret_cast<const float4 *>(tile_chunk(st, rr, cb * 8 + j));
-    y[4 * j] = f.x;
-    y[4 * j + 1] = f.y;
-    y[4 * j + 2] = f.z;
-    y[4 * j + 3] = f.w;
-  }
-  if (ROT == MX_K_ROT_RAND_SIGN) {
-    // the tile's 128 reduction indices need 32 Philox calls: lanes 0..31
-    // make one each, the sign bits meet in LDS as one nibble per call
-    if (lane < 32) sg[lane] = sign_nibble(q * 32 + lane, a.seed1_lo);
-    wave_lds_sync();
-    uint32_t mask = 0u;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) mask |= sg[cb * 8 + j] << (4 * j);
-    apply_sign_mask(y, mask);
-  }
-  rotate_block<ROT>(y);
-  // stochastic rounding index L = r * cols + kb * 32 + i (cols % 32 == 0)
-  const uint64_t q0 = (uint64_t)(r * a.cols + (kb << 5)) >> 2;
-  U4 w{0u, 0u, 0u, 0u};
-  auto u24_of = [&](int i) -> uint32_t {
-    if ((i & 3) == 0) w = sr_words(q0 + (uint64_t)(i >> 2), a.seed1_lo, a.seed1_hi);
-    return pick_word(w, (uint32_t)(i & 3)) >> 8;
-  };
-  constexpr int kWords = FMT == kFmtE4M3 ? 8 : 4;
-  uint32_t out[kWords];
-  uint32_t s = quantize_block<RotKind<ROT>::value, RND, FMT>(y, out, u24_of);
-  if (!valid) {                                           // padding: zero codes, scale code 0
-#pragma unroll
-    for (int j = 0; j < kWords; ++j) out[j] = 0u;
-    s = 0u;
-  }
-  const size_t tile = (size_t)g * nslices + q;
-  if constexpr (FMT == kFmtE4M3) {  // block cb of row rr: chunks 2 cb and 2 cb + 1
-    uint8_t *tp = a.codes1 + tile * 2048 + cb * 512 + rr * 16;
-    *reinterpret_cast<uint4 *>(tp) = make_uint4(out[0], out[1], out[2], out[3]);
-    *reinterpret_cast<uint4 *>(tp + 256) = make_uint4(out[4], out[5], out[6], out[7]);
-  } else {
-    *reinterpret_cast<uint4 *>(a.codes1 + tile * 1024 + lane * 16) =
-        make_uint4(out[0], out[1], out[2], out[3]);
-  }
-  a.scales1[scale_offset(r, kb, mnp)] = (uint8_t)s;
+// A double moved between lanes by one DPP control for both halves.
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xF, 0xF, false);
+  const uint32_t hi =
+      (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
+}
+constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E;         // quad_perm [1,0,3,2], [2,3,0,1]
+constexpr int kDppRor4 = 0x124, kDppRor8 = 0x128;       // row_ror within 16 lanes
+
+// Sums over the wave, four at once: lane l ends up with that of a[l % 4]. In
+// two steps a lane hands over what its neighbours keep (three values instead
+// of eight), the other four steps move one value.
+__device__ __forceinline__ double wave_row_sums(const double (&a)[4]) {
+  const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
+  const double p = (odd ? a[1] : a[0]) + dpp_f64<kDppXor1>(odd ? a[0] : a[1]);
+  const double q = (odd ? a[3] : a[2]) + dpp_f64<kDppXor1>(odd ? a[2] : a[3]);
+  double v = (high ? q : p) + dpp_f64<kDppXor2>(high ? p : q);
+  v += dpp_f64<kDppRor4>(v);
+  v += dpp_f64<kDppRor8>(v);
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
 }
 
-// ---------------------------------------------------------------------------
-// The axis-1 operand from h and rstd: a wave per tile, four per workgroup.
-// ---------------------------------------------------------------------------
-template <int F32, int ROT, int RND, int FMT>
-__global__ __launch_bounds__(256) void norm_axis1_kernel(NormArgs a) {
-  __shared__ __attribute__((aligned(16))) float stage[4][16 * 128];
-  __shared__ uint32_t signs[ROT == MX_K_ROT_RAND_SIGN ? 4 : 1][32];
-  const int64_t mnp = (a.rows + 255) & ~(int64_t)255;
-  const uint32_t nslices = (uint32_t)((a.cols + 127) >> 7);
-  const uint32_t ntiles = (uint32_t)(mnp >> 4) * nslices;
-  const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const uint32_t tile = blockIdx.x * 4u + (uint32_t)wv;
-  if (tile >= ntiles) return;
-  const uint32_t g = tile / nslices, q = tile - g * nslices;
-  float *st = stage[wv];
-  // lane l takes 8 columns of row 4 j + l / 16. Rows and columns past the
-  // source are read from its last row and last chunk: only padding uses them.
-  const int ch = lane & 15;
-  const int64_t k = min((int64_t)q * 128 + ch * 8, a.cols - 8);
-  float w8[8];
-  load_weight8(a.weight, a.wf32, k, w8);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int rr = j * 4 + (lane >> 4);
-    const int64_t r = min((int64_t)g * 16 + rr, a.rows - 1);
-    float v[8];
-    widen8<F32>(load8<F32>(a.h, r * a.ldh + k), v);
-    const float rs = a.rstd[r];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], rs), w8[i]);
-    *reinterpret_cast<float4 *>(tile_chunk(st, rr, 2 * ch)) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4 *>(tile_chunk(st, rr, 2 * ch + 1)) =
-        make_float4(v[4], v[5], v[6], v[7]);
+// Weights as they lie in memory, loaded ahead of their use.
+__device__ __forceinline__ Row8<1> load_weight_raw(const void *w, int f32, int64_t i) {
+  if (f32) return load8<1>(w, i);
+  Row8<1> r;
+  r.w[0] = load8<0>(w, i).w[0];
+  r.w[1] = r.w[0];
+  return r;
+}
+
+__device__ __forceinline__ void widen_weight(const Row8<1> &r, int f32, float (&v)[8]) {
+  if (f32) {
+    widen8<1>(r, v);
+  } else {
+    Row8<0> b;
+    b.w[0] = r.w[0];
+    widen8<0>(b, v);
   }
-  wave_lds_sync();
-  encode_tile<ROT, RND, FMT>(a, st, signs[ROT == MX_K_ROT_RAND_SIGN ? wv : 0], g, q, nslices, mnp);
+}
+
+template <int F32, int ROT, int RND, int FMT, int MAXW>
+__global__ __launch_bounds__(MAXW * 64, 4) void norm_axis1_kernel(NormArgs a) {
+  constexpr int kWords = FMT == kFmtE4M3 ? 8 : 4;
+  __shared__ __attribute__((aligned(16))) float stage[MAXW][kRows * kUnitCols];
+  __shared__ uint8_t signs[ROT == MX_K_ROT_RAND_SIGN ? MAXW : 1][kUnitCols / 4];
+  __shared__ double part[MAXW][kRows];
+  const int waves = blockDim.x >> 6, wv = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t mnp = (a.rows + 255) & ~(int64_t)255;
+  const uint32_t nblocks = (uint32_t)((a.cols + 127) >> 7) * 4;      // padding included
+  const uint32_t nunits = (nblocks + kUnitBlocks - 1) / kUnitBlocks;
+  const int64_t r0 = (int64_t)blockIdx.x * kRows;
+  // this lane's row and block of a unit, and where its codes and scales go
+  // (below 1 GiB: 32-bit offsets); block kb of a row adds a tile's bytes per
+  // slice and a quarter tile per block
+  const int er = lane % kRows, eb = lane / kRows;
+  const uint32_t m = (uint32_t)(r0 + er);
+  const uint32_t codes_row = (m >> 4) * (nblocks * (kWords * 64u)) + (m & 15) * 16u;
+  const uint32_t scales_row = (m >> 8) * 1024u + ((m >> 6) & 3) * 256u + (m & 15) * 4u + ((m >> 4) & 3);
+  const uint32_t panels = (uint32_t)(mnp >> 8);
+  auto put = [&](uint32_t kb, const uint32_t(&out)[kWords], uint32_t s) {
+    uint8_t *p = a.codes1 + (codes_row + (kb >> 2) * (kWords * 256u) + (kb & 3) * (kWords * 64u));
+    *reinterpret_cast<uint4 *>(p) = make_uint4(out[0], out[1], out[2], out[3]);
+    if constexpr (FMT == kFmtE4M3)      // the block's second 16-element chunk
+      *reinterpret_cast<uint4 *>(p + 256) = make_uint4(out[4], out[5], out[6], out[7]);
+    a.scales1[scales_row + (kb >> 2) * panels * 1024u + (kb & 3) * 64u] = (uint8_t)s;
+  };
+  if (r0 >= a.rows) {                                   // padding: zero codes, scale code 0
+    uint32_t out[kWords];
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) out[j] = 0u;
+    for (uint32_t u = wv; u < nunits; u += waves)
+      if (u * kUnitBlocks + eb < nblocks) put(u * kUnitBlocks + eb, out, 0u);
+    return;
+  }
+  // a lane loads 8 columns of each row. Rows past the last are read from the
+  // last row and not written; columns past the last are not read, and the
+  // blocks there are padding.
+  double acc[4] = {0.0, 0.0, 0.0, 0.0};
+  auto read_unit = [&](uint32_t u, Row8<F32>(&v)[4]) {
+    const int64_t k = (int64_t)u * kUnitCols + lane * 8;
+    if (k >= a.cols) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = load8<F32>(a.x, min(r0 + j, a.rows - 1) * a.ldx + k);
+    if (a.residual) {
+      Row8<F32> t[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        t[j] = load8<F32>(a.residual, min(r0 + j, a.rows - 1) * a.ldr + k);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = add_rows<F32>(v[j], t[j]);
+        if (r0 + j < a.rows) store8<F32>(a.h, (r0 + j) * a.ldh + k, v[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float f[8];
+      widen8<F32>(v[j], f);
+      acc[j] = add_squares(acc[j], f);
+    }
+  };
+  auto column = [&](uint32_t u) { return min((int64_t)u * kUnitCols + lane * 8, a.cols - 8); };
+  Row8<F32> held[4];
+  const Row8<1> w_held = load_weight_raw(a.weight, a.wf32, column(wv));
+  if (wv < (int)nunits) read_unit(wv, held);
+  for (uint32_t u = wv + waves; u < nunits; u += waves) {
+    Row8<F32> v[4];
+    read_unit(u, v);
+  }
+
+  // row sums over the waves; every wave works out rstd of row l % 4 in lane l
+  const double mine = wave_row_sums(acc);
+  if (lane < kRows) part[wv][lane] = mine;
+  __syncthreads();
+  double sum = 0.0;
+  for (int i = 0; i < waves; ++i) sum += part[i][er];
+  const float rs_er = rstd_of(sum, a.inv_cols, a.eps);
+  if (wv == 0 && lane < kRows && r0 + lane < a.rows) a.rstd[r0 + lane] = rs_er;
+  float rs[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    rs[j] = bits_f((uint32_t)__builtin_amdgcn_readlane((int)f_bits(rs_er), j));
+
+  // The 16-byte chunk c of row r of a unit lies at chunk c ^ f of the row,
+  // f = (r + 4 * (c / 16)) % 8, so that the 16 lanes that read a chunk of four
+  // rows' four blocks touch distinct banks.
+  float *st = stage[wv];
+  auto chunk = [&](int r, int c) { return st + r * kUnitCols + ((c ^ ((r + 4 * (c >> 4)) & 7)) << 2); };
+  uint8_t *sg = signs[ROT == MX_K_ROT_RAND_SIGN ? wv : 0];
+  auto encode = [&](uint32_t u, const Row8<F32>(&h)[4], const Row8<1> &w) {
+    wave_lds_sync();                                    // the unit before is read
+    float w8[8];
+    widen_weight(w, a.wf32, w8);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float v[8];
+      widen8<F32>(h[j], v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], rs[j]), w8[i]);
+      *reinterpret_cast<float4 *>(chunk(j, 2 * lane)) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4 *>(chunk(j, 2 * lane + 1)) = make_float4(v[4], v[5], v[6], v[7]);
+    }
+    // the unit's reduction indices need kUnitCols / 4 sign calls; the bits meet in
+    // LDS as one nibble per call
+    if (ROT == MX_K_ROT_RAND_SIGN)
+      for (int i = lane; i < kUnitCols / 4; i += 64)
+        sg[i] = (uint8_t)sign_nibble(u * (kUnitCols / 4) + i, a.seed1_lo);
+    wave_lds_sync();
+    const uint32_t kb = u * kUnitBlocks + eb;
+    if (kb >= nblocks) return;                          // past the operand's K extent
+    float y[32];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float4 f = *reinterpret_cast<const float4 *>(chunk(er, eb * 8 + j));
+      y[4 * j] = f.x;
+      y[4 * j + 1] = f.y;
+      y[4 * j + 2] = f.z;
+      y[4 * j + 3] = f.w;
+    }
+    if (ROT == MX_K_ROT_RAND_SIGN) {
+      uint32_t mask = 0u;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mask |= (uint32_t)sg[eb * 8 + j] << (4 * j);
+      apply_sign_mask(y, mask);
+    }
+    rotate_block<ROT>(y);
+    // stochastic rounding index L = r * cols + kb * 32 + i (cols % 32 == 0)
+    const uint64_t q0 = (uint64_t)((r0 + er) * a.cols + ((int64_t)kb << 5)) >> 2;
+    U4 words{0u, 0u, 0u, 0u};
+    auto u24_of = [&](int i) -> uint32_t {
+      if ((i & 3) == 0) words = sr_words(q0 + (uint64_t)(i >> 2), a.seed1_lo, a.seed1_hi);
+      return pick_word(words, (uint32_t)(i & 3)) >> 8;
+    };
+    uint32_t out[kWords];
+    uint32_t s = quantize_block<RotKind<ROT>::value, RND, FMT>(y, out, u24_of);
+    if (r0 + er >= a.rows || ((int64_t)kb << 5) >= a.cols) {   // padding
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) out[j] = 0u;
+      s = 0u;
+    }
+    put(kb, out, s);
+  };
+  if (wv < (int)nunits) encode(wv, held, w_held);
+  for (uint32_t u = wv + waves; u < nunits; u += waves) {
+    const Row8<1> w = load_weight_raw(a.weight, a.wf32, column(u));
+    Row8<F32> v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = load8<F32>(a.h, min(r0 + j, a.rows - 1) * a.ldh + column(u));
+    encode(u, v, w);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -206,22 +324,27 @@ __global__ __launch_bounds__(256) void norm_dual_kernel(NormArgs a, int64_t gx) 
   const bool rows_live = R0 < a.rows;
 
   if (rows_live) {
-    // lane (r0, ch) takes 8 columns of rows r0 and r0 + 16
+    // lane (r0, ch) takes 8 columns of rows r0 and r0 + 16, everything in
+    // flight at once; columns past the last are read from the last ones, which
+    // only padding sees
     const int ch = tid & 15, r0 = tid >> 4;
-    const int64_t c = C0 + 8 * ch;
-    float w8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (c < a.cols) load_weight8(a.weight, a.wf32, c, w8);
+    const int64_t c = min(C0 + 8 * ch, a.cols - 8);
+    const Row8<1> w = load_weight_raw(a.weight, a.wf32, c);
+    Row8<F32> h[2];
+    float rs[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) h[j] = load8<F32>(a.h, (R0 + r0 + 16 * j) * a.ldh + c);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) rs[j] = a.rstd[R0 + r0 + 16 * j];
+    float w8[8];
+    widen_weight(w, a.wf32, w8);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int rr = r0 + 16 * j;
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (c < a.cols) {
-        widen8<F32>(load8<F32>(a.h, (R0 + rr) * a.ldh + c), v);
-        const float rs = a.rstd[R0 + rr];
+      float v[8];
+      widen8<F32>(h[j], v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], rs), w8[i]);
-      }
-      float *d = st + rr * 132 + 8 * ch;
+      for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], rs[j]), w8[i]);
+      float *d = st + (r0 + 16 * j) * 132 + 8 * ch;
       *reinterpret_cast<float4 *>(d) = make_float4(v[0], v[1], v[2], v[3]);
       *reinterpret_cast<float4 *>(d + 4) = make_float4(v[4], v[5], v[6], v[7]);
     }
@@ -312,15 +435,17 @@ __global__ __launch_bounds__(256) void norm_dual_kernel(NormArgs a, int64_t gx) 
 
 template <int F32, int ROT, int RND, int FMT>
 hipError_t launch_norm(const NormArgs &a, hipStream_t stream) {
+  const int64_t mnp = (a.rows + 255) & ~(int64_t)255;
+  if (a.codes0 == nullptr) {
+    const int waves = (int)std::min<int64_t>(16, (a.cols + kUnitCols - 1) / kUnitCols);
+    const dim3 grid((unsigned)(mnp / kRows));
+    if (waves <= 8)
+      return launch(norm_axis1_kernel<F32, ROT, RND, FMT, 8>, grid, dim3(waves * 64), 0, stream, a);
+    return launch(norm_axis1_kernel<F32, ROT, RND, FMT, 16>, grid, dim3(waves * 64), 0, stream, a);
+  }
   const hipError_t e =
       launch(norm_rows_kernel<F32>, dim3((unsigned)a.rows), dim3(256), 0, stream, a);
   if (e != hipSuccess) return e;
-  const int64_t mnp = (a.rows + 255) & ~(int64_t)255;
-  if (a.codes0 == nullptr) {
-    const int64_t ntiles = (mnp >> 4) * ((a.cols + 127) >> 7);
-    return launch(norm_axis1_kernel<F32, ROT, RND, FMT>, dim3((unsigned)((ntiles + 3) / 4)),
-                  dim3(256), 0, stream, a);
-  }
   // columns up to the axis-0 operand's padded MN extent, rows up to the axis-1
   // operand's (each covers the other operand's K extent)
   const int64_t gx = ((a.cols + 255) & ~(int64_t)255) / 128;
