@@ -490,7 +490,7 @@ mx_status mx_rmsnorm_backward_workspace(int64_t rows, int64_t cols, size_t *byte
   if (bytes == nullptr) return MX_ERR_NULL;
   if (rows < 0 || cols < 0) return MX_ERR_SHAPE;
   if (extents_too_large(rows, cols)) return MX_ERR_UNSUPPORTED;
-  *bytes = (size_t)mx::norm_grad_groups(rows) * (size_t)cols * sizeof(float);
+  *bytes = (size_t)mx::norm_grad_groups(rows, cols) * (size_t)cols * sizeof(float);
   return MX_OK;
 }
 

@@ -132,14 +132,23 @@ struct NormGradArgs {
   const void *weight;              // [cols]
   void *dh;                        // [rows, cols]
   float *dweight;                  // [cols]
-  float *partial;                  // [norm_grad_groups(rows)][cols]
+  float *partial;                  // [norm_grad_groups(rows, cols)][cols]
   int64_t rows, cols, lddy, ldh, ldres, lddh;
   int f32, wf32;
 };
 
-// Workgroups of the gradient's row pass, one partial weight gradient each. A
-// function of the shape alone, so that the order of the sums is too.
-inline int norm_grad_groups(int64_t rows) { return (int)(rows < 512 ? rows : 512); }
+// Workgroups of the gradient's row pass, one partial weight gradient each: 16
+// waves to a compute unit where that leaves each at least eight rows, up to 512
+// workgroups of them where there are fewer rows. A function of the shape alone, so
+// that the order of the sums is too.
+inline int norm_grad_groups(int64_t rows, int64_t cols) {
+  const int64_t waves = cols >= 16 * 512 ? 16 : (cols + 511) / 512;
+  const int64_t full = waves > 0 ? 4096 / waves : 4096;
+  const int64_t some = full < rows / 8 ? full : rows / 8;
+  const int64_t low = full < 512 ? full : 512;
+  const int64_t most = some > low ? some : low;
+  return (int)(rows < most ? rows : most);
+}
 
 hipError_t norm_grad_launch(const NormGradArgs &a, hipStream_t stream);
 

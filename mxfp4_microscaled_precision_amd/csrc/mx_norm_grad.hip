@@ -37,58 +37,75 @@ __device__ __forceinline__ float group_sum(float v, float *part, int waves) {
 }
 
 // V units of eight columns per thread cover a row in one go; wider rows take
-// norm_grad_wide_kernel.
+// norm_grad_wide_kernel. The next row's loads are in flight while the
+// workgroup adds up this one's products.
 template <int F32, int V>
 __global__ __launch_bounds__(1024) void norm_grad_kernel(NormGradArgs a) {
   __shared__ float part[2][16];
   const int waves = blockDim.x >> 6;
   const float inv_n = 1.0f / (float)a.cols;
   float w[V][8], dw[V][8];
+  int64_t col[V];
+  bool live[V];
 #pragma unroll
   for (int u = 0; u < V; ++u) {
     const int64_t c = ((int64_t)u * blockDim.x + threadIdx.x) * 8;
+    live[u] = c < a.cols;
+    col[u] = min(c, a.cols - 8);       // threads past the row read its end and count nothing
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[u][i] = dw[u][i] = 0.f;
-    if (c < a.cols) load_weight8(a.weight, a.wf32, c, w[u]);
+    if (live[u]) load_weight8(a.weight, a.wf32, c, w[u]);
   }
-  int flip = 0;
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, flip ^= 1) {
-    const float rs = a.rstd[r];
-    float xh[V][8], dy[V][8];
-    float dot = 0.f;
+  Row8<F32> h[V], dy[V], res[V];
+  float rs;
+  auto read = [&](int64_t r) {
+    rs = a.rstd[r];
 #pragma unroll
     for (int u = 0; u < V; ++u) {
-      const int64_t c = ((int64_t)u * blockDim.x + threadIdx.x) * 8;
-      if (c < a.cols) {
-        widen8<F32>(load8<F32>(a.h, r * a.ldh + c), xh[u]);
-        widen8<F32>(load8<F32>(a.dy, r * a.lddy + c), dy[u]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          xh[u][i] *= rs;
-          dw[u][i] = __fmaf_rn(dy[u][i], xh[u][i], dw[u][i]);
-          dy[u][i] *= w[u][i];
-          dot = __fmaf_rn(dy[u][i], xh[u][i], dot);
-        }
-      }
+      h[u] = load8_once<F32>(a.h, r * a.ldh + col[u]);
+      dy[u] = load8_once<F32>(a.dy, r * a.lddy + col[u]);
+      if (a.dres) res[u] = load8_once<F32>(a.dres, r * a.ldres + col[u]);
     }
+  };
+  int flip = 0;
+  int64_t r = blockIdx.x;
+  read(r);
+  for (; r < a.rows; r += gridDim.x, flip ^= 1) {
+    float xh[V][8], g[V][8];
+    Row8<F32> o[V];
+    float dot = 0.f;
+    const float s = rs;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      widen8<F32>(h[u], xh[u]);
+      widen8<F32>(dy[u], g[u]);
+      o[u] = res[u];
+      float d = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        xh[u][i] *= s;
+        dw[u][i] = __fmaf_rn(g[u][i], xh[u][i], dw[u][i]);
+        g[u][i] *= w[u][i];
+        d = __fmaf_rn(g[u][i], xh[u][i], d);
+      }
+      dot += live[u] ? d : 0.f;
+    }
+    read(min(r + gridDim.x, a.rows - 1));
     const float m = group_sum(dot, part[flip], waves) * inv_n;
 #pragma unroll
     for (int u = 0; u < V; ++u) {
-      const int64_t c = ((int64_t)u * blockDim.x + threadIdx.x) * 8;
-      if (c < a.cols) {
-        float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (a.dres) widen8<F32>(load8<F32>(a.dres, r * a.ldres + c), o);
+      if (live[u]) {
+        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (a.dres) widen8<F32>(o[u], f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = __fmaf_rn(__fmaf_rn(xh[u][i], -m, dy[u][i]), rs, o[i]);
-        store8<F32>(a.dh, r * a.lddh + c, narrow8<F32>(o));
+        for (int i = 0; i < 8; ++i) f[i] = __fmaf_rn(__fmaf_rn(xh[u][i], -m, g[u][i]), s, f[i]);
+        store8<F32>(a.dh, r * a.lddh + col[u], narrow8<F32>(f));
       }
     }
   }
 #pragma unroll
-  for (int u = 0; u < V; ++u) {
-    const int64_t c = ((int64_t)u * blockDim.x + threadIdx.x) * 8;
-    if (c < a.cols) store8<1>(a.partial, (int64_t)blockIdx.x * a.cols + c, narrow8<1>(dw[u]));
-  }
+  for (int u = 0; u < V; ++u)
+    if (live[u]) store8<1>(a.partial, (int64_t)blockIdx.x * a.cols + col[u], narrow8<1>(dw[u]));
 }
 
 // Rows of any width: two passes over the row, the second from cache, and the
@@ -134,36 +151,54 @@ __global__ __launch_bounds__(1024) void norm_grad_wide_kernel(NormGradArgs a) {
   }
 }
 
-// dweight[c] = sum of the partial rows, in 64 bits: 64 columns per workgroup,
-// four waves share the rows.
-__global__ __launch_bounds__(256) void norm_grad_sum_kernel(const float *partial, int groups,
-                                                            int64_t cols, float *dweight) {
-  __shared__ double part[4][64];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+// dweight[c] = sum of the partial rows, in 64 bits: 32 columns per workgroup,
+// 32 threads to a column, all of a thread's loads in flight together.
+__global__ __launch_bounds__(1024) void norm_grad_sum_kernel(const float *partial, int groups,
+                                                             int64_t cols, float *dweight) {
+  __shared__ double part[32][33];
+  const int c = threadIdx.x & 31, t = threadIdx.x >> 5;
+  const int64_t col = (int64_t)blockIdx.x * 32 + c;
   double s = 0.0;
-  if (c < cols)
-    for (int g = wv; g < groups; g += 4) s += (double)partial[(int64_t)g * cols + c];
-  part[wv][lane] = s;
+  if (col < cols) {
+    const float *p = partial + col;
+    int g = t;
+    for (; g + 7 * 32 < groups; g += 8 * 32) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = p[(int64_t)(g + i * 32) * cols];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += (double)v[i];
+    }
+    for (; g < groups; g += 32) s += (double)p[(int64_t)g * cols];
+  }
+  part[t][c] = s;
   __syncthreads();
-  if (wv == 0 && c < cols)
-    dweight[c] = (float)((part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]));
+  // thread (t, c) takes row c of column t: half a wave adds a column up
+  double v = part[c][t];
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) v += __shfl_xor(v, m);
+  if (c == 0 && (int64_t)blockIdx.x * 32 + t < cols) dweight[(int64_t)blockIdx.x * 32 + t] = (float)v;
 }
 
+// One unit of eight columns per thread up to 8192 columns, two of bf16 rows up
+// to 16384 (2048 x 12288: 53 us, in two passes 81 us); fp32 rows would spill
+// there (198 us against 120 us) and take the two passes.
 template <int F32>
 hipError_t launch_grad(const NormGradArgs &a, hipStream_t stream) {
-  const int64_t units = (a.cols + 7) / 8;
+  const int64_t units = a.cols / 8;
   const int threads = (int)std::min<int64_t>(1024, (units + 63) / 64 * 64);
-  const dim3 grid((unsigned)norm_grad_groups(a.rows));
-  hipError_t e = hipSuccess;
-  if (a.rows == 0)
-    e = hipSuccess;                                    // the sum below writes zeros
-  else if (units <= threads)
-    e = launch(norm_grad_kernel<F32, 1>, grid, dim3(threads), 0, stream, a);
-  else
-    e = launch(norm_grad_wide_kernel<F32>, grid, dim3(threads), 0, stream, a);
+  const dim3 grid((unsigned)norm_grad_groups(a.rows, a.cols));
+  hipError_t e = hipSuccess;                           // without rows the sum writes zeros
+  if (a.rows > 0) {
+    if (units <= threads)
+      e = launch(norm_grad_kernel<F32, 1>, grid, dim3(threads), 0, stream, a);
+    else if (!F32 && units <= 2 * threads)
+      e = launch(norm_grad_kernel<0, 2>, grid, dim3(threads), 0, stream, a);
+    else
+      e = launch(norm_grad_wide_kernel<F32>, grid, dim3(threads), 0, stream, a);
+  }
   if (e != hipSuccess) return e;
-  return launch(norm_grad_sum_kernel, dim3((unsigned)((a.cols + 63) / 64)), dim3(256), 0, stream,
+  return launch(norm_grad_sum_kernel, dim3((unsigned)((a.cols + 31) / 32)), dim3(1024), 0, stream,
                 a.partial, (int)grid.x, a.cols, a.dweight);
 }
 
