@@ -612,6 +612,9 @@ mx::GradTable grad_table(const mx_grad_set *s) {
                                                        (size_t)s->count * sizeof(mx::GradTensor));
   t.chunks = s->chunks;
   t.chunk = s->chunk;
+  t.bytes = 0;
+  t.once = s->chunks;
+  for (int32_t i = 0; i < s->count; ++i) t.bytes += grad_bytes(s->grads[i]);
   return t;
 }
 

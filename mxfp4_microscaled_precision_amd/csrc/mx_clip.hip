@@ -25,47 +25,79 @@ namespace mx {
 namespace {
 
 constexpr int kThreads = 256;
+// Five workgroups to a compute unit (102 registers), which kGradGroups fills on
+// 256 of them.
+constexpr int kWavesPerSimd = 5;
+constexpr int64_t kInfinityCache = (int64_t)256 << 20;
 
-// Elements [0, n) of a contiguous run: f(index) for the lanes of a workgroup
-// in units of eight, then the last few one by one.
+// Tensor addresses come out of a table: said to be global memory, they are
+// not looked up as LDS or scratch first.
+typedef __attribute__((address_space(1))) uint8_t gbyte;
 typedef uint32_t any_u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+typedef __attribute__((address_space(1))) any_u32x4 g_u32x4;
 
-// Eight elements from any element-aligned address (gfx950 loads and stores 16
-// bytes at any alignment).
+// Sixteen bytes from any element-aligned address (gfx950 loads and stores them
+// at any alignment): 4 fp32 or 8 bf16 elements.
+// Stores, and loads with ONCE, are of data that is not read again here.
+template <bool ONCE>
+__device__ __forceinline__ any_u32x4 load16(const gbyte *p) {
+  const g_u32x4 *q = reinterpret_cast<const g_u32x4 *>(p);
+  return ONCE ? __builtin_nontemporal_load(q) : *q;
+}
+__device__ __forceinline__ void store16(gbyte *p, any_u32x4 v) {
+  __builtin_nontemporal_store(v, reinterpret_cast<g_u32x4 *>(p));
+}
+
 template <int F32>
-__device__ __forceinline__ Row8<F32> load_any8(const uint8_t *p) {
-  Row8<F32> r;
+constexpr int unit_elems() { return F32 ? 4 : 8; }
+
+template <int F32>
+__device__ __forceinline__ void widen16(any_u32x4 r, float (&v)[unit_elems<F32>()]) {
 #pragma unroll
-  for (int k = 0; k < (F32 ? 2 : 1); ++k) r.w[k] = reinterpret_cast<const any_u32x4 *>(p)[k];
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (F32) {
+      v[i] = bits_f(r[i]);
+    } else {
+      v[2 * i] = bits_f(r[i] << 16);
+      v[2 * i + 1] = bits_f(r[i] & 0xFFFF0000u);
+    }
+  }
+}
+
+template <int F32>
+__device__ __forceinline__ any_u32x4 narrow16(const float (&v)[unit_elems<F32>()]) {
+  any_u32x4 r;
+  if constexpr (F32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = f_bits(v[i]);
+  } else {
+    r = narrow8<0>(v).w[0];
+  }
   return r;
 }
 
 template <int F32>
-__device__ __forceinline__ void store_any8(uint8_t *p, const Row8<F32> &r) {
-#pragma unroll
-  for (int k = 0; k < (F32 ? 2 : 1); ++k) reinterpret_cast<any_u32x4 *>(p)[k] = r.w[k];
+__device__ __forceinline__ float load_one(const gbyte *p) {
+  if (F32) return *reinterpret_cast<const __attribute__((address_space(1))) float *>(p);
+  return bits_f((uint32_t)*reinterpret_cast<const __attribute__((address_space(1))) uint16_t *>(p)
+                << 16);
 }
 
 template <int F32>
-__device__ __forceinline__ float load_one(const uint8_t *p) {
-  if (F32) return *reinterpret_cast<const float *>(p);
-  return bits_f((uint32_t)*reinterpret_cast<const uint16_t *>(p) << 16);
-}
-
-template <int F32>
-__device__ __forceinline__ void store_one(uint8_t *p, float v) {
+__device__ __forceinline__ void store_one(gbyte *p, float v) {
   if constexpr (F32) {
-    *reinterpret_cast<float *>(p) = v;
+    *reinterpret_cast<__attribute__((address_space(1))) float *>(p) = v;
   } else {
     const float f[8] = {v, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    *reinterpret_cast<uint16_t *>(p) = (uint16_t)narrow8<0>(f).w[0][0];
+    *reinterpret_cast<__attribute__((address_space(1))) uint16_t *>(p) =
+        (uint16_t)narrow8<0>(f).w[0][0];
   }
 }
 
 // A chunk's elements as contiguous runs: the whole chunk of a tensor without
 // gaps, else the piece of each row. f(first element within the tensor's
-// buffer, elements, thread, threads); a run of a tensor with gaps goes to one
-// wave, a whole chunk to the workgroup.
+// buffer, within the tensor, elements, thread, threads); a run of a tensor
+// with gaps goes to one wave, a whole chunk to the workgroup.
 template <typename F>
 __device__ __forceinline__ void for_runs(const GradTensor &t, int64_t ld, int64_t first,
                                          int64_t len, F f) {
@@ -81,39 +113,58 @@ __device__ __forceinline__ void for_runs(const GradTensor &t, int64_t ld, int64_
   }
 }
 
-template <int F32>
-__device__ __forceinline__ double run_squares(const uint8_t *p, int64_t len, int tid, int threads) {
+// A thread's 16-byte units of a run, kBatch of them in flight at a time: f of
+// each unit's offset (bytes) and contents; then one element each of the last
+// few to g. (Starting the units at the run's first 16-byte boundary instead
+// gained nothing on tensors packed without alignment.)
+constexpr int kBatch = 4;
+
+template <int F32, bool ONCE, typename F, typename G>
+__device__ __forceinline__ void for_units(const gbyte *p, int len, int tid, int threads, F f, G g) {
   constexpr int kSize = F32 ? 4 : 2;
-  double acc = 0.0;
-  const int64_t whole = len & ~(int64_t)7;
-  for (int64_t i = tid * 8; i < whole; i += threads * 8) {
-    float v[8];
-    widen8<F32>(load_any8<F32>(p + i * kSize), v);
+  const int whole = (len * kSize) & ~15, step = threads * 16;
+  int i = tid * 16;
+  for (; i + (kBatch - 1) * step < whole; i += kBatch * step) {
+    any_u32x4 v[kBatch];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) acc = __builtin_fma((double)v[k], (double)v[k], acc);
+    for (int b = 0; b < kBatch; ++b) v[b] = load16<ONCE>(p + (uint32_t)(i + b * step));
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) f(i + b * step, v[b]);
   }
-  if (tid < len - whole) {
-    const double v = (double)load_one<F32>(p + (whole + tid) * kSize);
-    acc = __builtin_fma(v, v, acc);
-  }
+  for (; i < whole; i += step) f(i, load16<ONCE>(p + (uint32_t)i));
+  i = whole + tid * kSize;
+  if (i < len * kSize) g(i, load_one<F32>(p + (uint32_t)i));
+}
+
+template <int F32, bool ONCE>
+__device__ __forceinline__ double run_squares(const gbyte *p, int len, int tid, int threads) {
+  double acc = 0.0;
+  for_units<F32, ONCE>(
+      p, len, tid, threads,
+      [&](int, any_u32x4 r) {
+        float v[unit_elems<F32>()];
+        widen16<F32>(r, v);
+#pragma unroll
+        for (int k = 0; k < unit_elems<F32>(); ++k)
+          acc = __builtin_fma((double)v[k], (double)v[k], acc);
+      },
+      [&](int, float v) { acc = __builtin_fma((double)v, (double)v, acc); });
   return acc;
 }
 
-template <int F32>
-__device__ __forceinline__ void run_scale(const uint8_t *p, uint8_t *o, int64_t len, int tid,
-                                          int threads, float coef) {
-  constexpr int kSize = F32 ? 4 : 2;
-  const int64_t whole = len & ~(int64_t)7;
-  for (int64_t i = tid * 8; i < whole; i += threads * 8) {
-    float v[8];
-    widen8<F32>(load_any8<F32>(p + i * kSize), v);
+template <int F32, bool ONCE>
+__device__ __forceinline__ void run_scale(const gbyte *p, gbyte *o, int len, int tid, int threads,
+                                          float coef) {
+  for_units<F32, ONCE>(
+      p, len, tid, threads,
+      [&](int i, any_u32x4 r) {
+        float v[unit_elems<F32>()];
+        widen16<F32>(r, v);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = __fmul_rn(v[k], coef);
-    store_any8<F32>(o + i * kSize, narrow8<F32>(v));
-  }
-  if (tid < len - whole)
-    store_one<F32>(o + (whole + tid) * kSize,
-                   __fmul_rn(load_one<F32>(p + (whole + tid) * kSize), coef));
+        for (int k = 0; k < unit_elems<F32>(); ++k) v[k] = __fmul_rn(v[k], coef);
+        store16(o + (uint32_t)i, narrow16<F32>(v));
+      },
+      [&](int i, float v) { store_one<F32>(o + (uint32_t)i, __fmul_rn(v, coef)); });
 }
 
 __device__ __forceinline__ double group_sum(double v, double *part) {
@@ -134,17 +185,38 @@ __device__ __forceinline__ double total_of(const double *partial, int groups, do
   return group_sum(s, part);
 }
 
-__global__ __launch_bounds__(kThreads) void grad_squares_kernel(GradTable t, double *partial) {
+// Chunk k of a table: its tensor, its place in it, and how many elements.
+struct Chunk {
+  GradTensor t;
+  uint32_t tensor;
+  int64_t first, len;
+};
+
+__device__ __forceinline__ Chunk chunk_at(const GradTable &t, int64_t k) {
+  const GradChunk c = t.chunk_of[k];
+  Chunk r;
+  r.t = t.tensors[c.tensor];
+  r.tensor = c.tensor;
+  r.first = (int64_t)c.at * t.chunk;
+  r.len = min(t.chunk, r.t.rows * r.t.cols - r.first);
+  return r;
+}
+
+__global__ __launch_bounds__(kThreads, kWavesPerSimd) void grad_squares_kernel(GradTable t, double *partial) {
   __shared__ double part[kThreads / 64];
   double acc = 0.0;
+  Chunk next = chunk_at(t, blockIdx.x);
   for (int64_t k = blockIdx.x; k < t.chunks; k += gridDim.x) {
-    const GradChunk c = t.chunk_of[k];
-    const GradTensor g = t.tensors[c.tensor];
-    const int64_t first = (int64_t)c.at * t.chunk, len = min(t.chunk, g.rows * g.cols - first);
-    const uint8_t *base = static_cast<const uint8_t *>(g.data);
-    for_runs(g, g.ld, first, len, [&](int64_t at, int64_t, int64_t n, int tid, int threads) {
-      acc += g.f32 ? run_squares<1>(base + at * 4, n, tid, threads)
-                   : run_squares<0>(base + at * 2, n, tid, threads);
+    const Chunk c = next;
+    next = chunk_at(t, min(k + gridDim.x, t.chunks - 1));   // looked up while this one is read
+    const gbyte *base = (const gbyte *)c.t.data;
+    for_runs(c.t, c.t.ld, c.first, c.len, [&](int64_t at, int64_t, int64_t n, int tid, int threads) {
+      if (k < t.once)
+        acc += c.t.f32 ? run_squares<1, true>(base + at * 4, (int)n, tid, threads)
+                       : run_squares<0, true>(base + at * 2, (int)n, tid, threads);
+      else
+        acc += c.t.f32 ? run_squares<1, false>(base + at * 4, (int)n, tid, threads)
+                       : run_squares<0, false>(base + at * 2, (int)n, tid, threads);
     });
   }
   const double s = group_sum(acc, part);
@@ -159,7 +231,7 @@ __global__ __launch_bounds__(kThreads) void grad_norm_kernel(const double *parti
 }
 
 // in and out describe the same shapes and types; they may be the same table.
-__global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradTable in, GradTable out,
+__global__ __launch_bounds__(kThreads, kWavesPerSimd) void grad_scale_kernel(GradTable in, GradTable out,
                                                               const double *partial, int groups,
                                                               float max_norm, float *norm) {
   __shared__ double part[kThreads / 64];
@@ -170,22 +242,24 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradTable in, Grad
   const double q = (double)max_norm / (n + 1e-6);
   const float coef = q > 1.0 ? 1.0f : (float)q;
   if (coef == 1.0f && in.tensors == out.tensors) return;   // nothing changes in place
+  const int64_t last = in.chunks - 1;
+  Chunk next = chunk_at(in, last - blockIdx.x);           // from the end, see grad_clip_launch
   for (int64_t k = blockIdx.x; k < in.chunks; k += gridDim.x) {
-    const GradChunk c = in.chunk_of[k];
-    const GradTensor g = in.tensors[c.tensor], o = out.tensors[c.tensor];
-    const int64_t first = (int64_t)c.at * in.chunk, len = min(in.chunk, g.rows * g.cols - first);
-    const uint8_t *src = static_cast<const uint8_t *>(g.data);
-    uint8_t *dst = static_cast<uint8_t *>(o.data);
+    const Chunk c = next;
+    const GradTensor g = c.t, o = out.tensors[c.tensor];
+    next = chunk_at(in, last - min(k + gridDim.x, last));
+    const gbyte *src = (const gbyte *)g.data;
+    gbyte *dst = (gbyte *)o.data;
     // runs without gaps on both sides: the input's, or where that has none the
     // output's
     const int64_t ld = g.ld == g.cols ? o.ld : g.ld;
-    for_runs(g, ld, first, len, [&](int64_t, int64_t e, int64_t m, int tid, int threads) {
+    for_runs(g, ld, c.first, c.len, [&](int64_t, int64_t e, int64_t m, int tid, int threads) {
       const int64_t r = ld == g.cols ? 0 : e / g.cols, col = e - r * g.cols;
       const int64_t is = ld == g.cols ? e : r * g.ld + col, os = ld == g.cols ? e : r * o.ld + col;
       if (g.f32)
-        run_scale<1>(src + is * 4, dst + os * 4, m, tid, threads, coef);
+        run_scale<1, true>(src + is * 4, dst + os * 4, (int)m, tid, threads, coef);
       else
-        run_scale<0>(src + is * 2, dst + os * 2, m, tid, threads, coef);
+        run_scale<0, true>(src + is * 2, dst + os * 2, (int)m, tid, threads, coef);
     });
   }
 }
@@ -202,10 +276,18 @@ hipError_t grad_norm_launch(const GradTable &t, double *partial, float *norm, hi
   return launch(grad_norm_kernel, dim3(1), dim3(kThreads), 0, stream, partial, groups, norm);
 }
 
-hipError_t grad_clip_launch(const GradTable &in, const GradTable &out, double *partial,
+hipError_t grad_clip_launch(const GradTable &all, const GradTable &out, double *partial,
                             float max_norm, float *norm, hipStream_t stream) {
-  const int groups = (int)std::min<int64_t>(in.chunks, kGradGroups);
-  if (groups == 0) return grad_norm_launch(in, partial, norm, stream);
+  const int groups = (int)std::min<int64_t>(all.chunks, kGradGroups);
+  if (groups == 0) return grad_norm_launch(all, partial, norm, stream);
+  // The norm's pass leaves the last 256 MB it reads in the Infinity cache and
+  // keeps what comes before out of it; the scaling starts from the end. Read
+  // without regard to that a block's gradients took 454 us (fp32) and 211 us
+  // (bf16) against 431 us and 208 us, with nothing kept 448 us and 219 us; the
+  // small sets that fit as a whole 138 us with nothing kept, 123 us with all.
+  GradTable in = all;
+  const double kept = (double)kInfinityCache / (double)in.bytes * (double)in.chunks;
+  in.once = in.chunks - (kept < (double)in.chunks ? (int64_t)kept : in.chunks);
   const hipError_t e =
       launch(grad_squares_kernel, dim3(groups), dim3(kThreads), 0, stream, in, partial);
   if (e != hipSuccess) return e;

@@ -165,9 +165,11 @@ struct GradTable {
   const GradTensor *tensors;
   const GradChunk *chunk_of;
   int64_t chunks, chunk;
+  int64_t bytes;                   // of all tensors
+  int64_t once;                    // chunks before this one are not read again soon
 };
 
-constexpr int kGradGroups = 2048;  // workgroups, and partial sums, at most
+constexpr int kGradGroups = 1280;  // workgroups, and partial sums, at most
 
 hipError_t grad_norm_launch(const GradTable &t, double *partial, float *norm, hipStream_t stream);
 hipError_t grad_clip_launch(const GradTable &in, const GradTable &out, double *partial,
