@@ -517,7 +517,8 @@ def _place(device, stream):
     still be using."""
     import torch
     if stream is None:
-        handle = torch.cuda.current_stream(device).cuda_stream
+        # torch.cuda.current_stream(device).cuda_stream without its stream object
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
         here = device.index == torch.cuda.current_device()
         return (_HERE if here else torch.cuda.device(device)), handle
     if not hasattr(stream, "cuda_stream"):
@@ -530,29 +531,32 @@ def _place(device, stream):
 
 def _row_dtype(t, name: str) -> int:
     import torch
-    if t.dtype == torch.bfloat16:
-        return OUT_DTYPES["bf16"]
-    if t.dtype == torch.float32:
-        return OUT_DTYPES["f32"]
+    dtype = t.dtype
+    if dtype is torch.bfloat16:
+        return 1
+    if dtype is torch.float32:
+        return 0
     raise ValueError(f"{name} must be bfloat16 or float32")
 
 
 def _rows_of(t, name: str, like=None) -> Tuple[Optional[int], int]:
     """(address, leading dimension) of a 2-D CUDA matrix with unit column
     stride, of like's type, shape and device."""
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA (HIP) tensor; there is no CPU path")
-    if like is not None and (t.dtype != like.dtype or t.shape != like.shape
+    if like is not None and (t.dtype is not like.dtype or shape != like.shape
                              or t.device != like.device):
         raise ValueError(f"{name} must have the type, shape and device of the other rows")
-    rows, cols = t.shape
+    rows, cols = shape
     if rows == 0 or cols == 0:
         return None, (cols + 7) // 8 * 8
-    if t.stride(1) != 1 and cols > 1:
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
-    return t.data_ptr(), t.stride(0) if rows > 1 else (cols + 7) // 8 * 8
+    return t.data_ptr(), ld if rows > 1 else (cols + 7) // 8 * 8
 
 
 def _vector(t, name: str, n: int, device):
@@ -585,45 +589,41 @@ def rmsnorm_quantize(x, weight, residual=None, eps: float = 1e-5, format: str = 
     returned as h where there is no residual.
     """
     import torch
-    lib = load_library()
-    n = NormDesc()
-    n.x, n.ldx = _rows_of(x, "x")
-    n.dtype = _row_dtype(x, "x")
+    lib = _lib or load_library()
+    xp, ldx = _rows_of(x, "x")
+    dtype, device = _row_dtype(x, "x"), x.device
     rows, cols = x.shape
-    n.rows, n.cols, n.eps = rows, cols, eps
-    n.weight = _vector(weight, "weight", cols, x.device)
-    n.weight_dtype = _row_dtype(weight, "weight")
-    sizes = quantize_fp8_sizes if FORMATS[format] else quantize_sizes
-    size1 = sizes(rows, cols, 1)
-    size0 = sizes(rows, cols, 0) if dual else (0, 0)
-    place, handle = _place(x.device, stream)
+    wp = _vector(weight, "weight", cols, device)
+    rp, ldr = (None, 0) if residual is None else _rows_of(residual, "residual", x)
+    fmt = FORMATS[format]
+    sizes = quantize_fp8_sizes if fmt else quantize_sizes
+    size = sizes(rows, cols, 1) + (sizes(rows, cols, 0) if dual else ())
+    place, handle = _place(device, stream)
     with place:
-        if residual is not None:
-            n.residual, n.ldr = _rows_of(residual, "residual", x)
-            if h is None:
-                h = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-            n.h, n.ldh = _rows_of(h, "h", x)
-        else:
+        if residual is None:
             if h is not None and h is not x:
                 raise ValueError("without a residual h is x itself")
-            h = x
-        rstd = torch.empty((rows,), dtype=torch.float32, device=x.device)
-        n.rstd = rstd.data_ptr() if rows else None
-        buf = [torch.empty((b,), dtype=torch.uint8, device=x.device)
-               for b in (size1 + size0 if dual else size1)]
-        ptr = [b.data_ptr() if b.numel() else None for b in buf]
+            h, hp, ldh = x, None, 0
+        elif h is None:
+            h = torch.empty((rows, cols), dtype=x.dtype, device=device)
+            hp, ldh = h.data_ptr(), cols
+        else:
+            hp, ldh = _rows_of(h, "h", x)
+        rstd = torch.empty(rows, dtype=torch.float32, device=device)
+        buf = [torch.empty(b, dtype=torch.uint8, device=device) for b in size]
+        ptr = [b.data_ptr() or None for b in buf] + [None, None]
+        n = NormDesc(xp, rp, wp, hp, rstd.data_ptr() or None, rows, cols, ldx, ldr, ldh, dtype,
+                     _row_dtype(weight, "weight"), eps)
         d1, d0 = QTensorDesc(), QTensorDesc()
-        st = lib.mx_rmsnorm_quantize(ctypes.byref(n), FORMATS[format], 32, ROTATE[rotate],
-                                     ROUND[round], seed1 & 0xFFFFFFFFFFFFFFFF,
-                                     seed0 & 0xFFFFFFFFFFFFFFFF, ptr[0], ptr[1],
-                                     ptr[2] if dual else None, ptr[3] if dual else None,
-                                     ctypes.byref(d1), ctypes.byref(d0), handle)
+        st = lib.mx_rmsnorm_quantize(n, fmt, 32, ROTATE[rotate], ROUND[round],
+                                     seed1 & 0xFFFFFFFFFFFFFFFF, seed0 & 0xFFFFFFFFFFFFFFFF,
+                                     ptr[0], ptr[1], ptr[2], ptr[3], d1, d0, handle)
     _check(st, "mx_rmsnorm_quantize")
     if not dual:
         return RMSNormQuantized(QTensor(buf[0], buf[1], d1), None, h, rstd)
     if not (rows and cols):     # empty operands have no buffers to tell the call by
         d0 = QTensorDesc(None, None, rows, cols, 0, 32, ROTATE[rotate], ROUND[round],
-                         seed0 & 0xFFFFFFFFFFFFFFFF, FORMATS[format])
+                         seed0 & 0xFFFFFFFFFFFFFFFF, fmt)
     return RMSNormQuantized(QTensor(buf[0], buf[1], d1), QTensor(buf[2], buf[3], d0), h, rstd)
 
 
@@ -633,33 +633,31 @@ def rmsnorm_backward(dy, h, rstd, weight, dres=None, dh=None, stream=None):
     the gradient that reaches h past the norm. dh is the gradient of x and of
     residual; it may be written over dy or dres. dweight is fp32."""
     import torch
-    lib = load_library()
-    g = NormGradDesc()
-    g.dy, g.lddy = _rows_of(dy, "dy")
-    g.dtype = _row_dtype(dy, "dy")
+    lib = _lib or load_library()
+    yp, lddy = _rows_of(dy, "dy")
+    dtype, device = _row_dtype(dy, "dy"), dy.device
     rows, cols = dy.shape
-    g.rows, g.cols = rows, cols
-    g.h, g.ldh = _rows_of(h, "h", dy)
-    if dres is not None:
-        g.dres, g.ldres = _rows_of(dres, "dres", dy)
-    if rstd.dtype != torch.float32:
+    hp, ldh = _rows_of(h, "h", dy)
+    rp, ldres = (None, 0) if dres is None else _rows_of(dres, "dres", dy)
+    if rstd.dtype is not torch.float32:
         raise ValueError("rstd must be float32")
-    g.rstd = _vector(rstd, "rstd", rows, dy.device)
-    g.weight = _vector(weight, "weight", cols, dy.device)
-    g.weight_dtype = _row_dtype(weight, "weight")
+    sp = _vector(rstd, "rstd", rows, device)
+    wp = _vector(weight, "weight", cols, device)
     need = ctypes.c_size_t()
-    _check(lib.mx_rmsnorm_backward_workspace(rows, cols, ctypes.byref(need)),
-           "mx_rmsnorm_backward_workspace")
-    place, handle = _place(dy.device, stream)
+    _check(lib.mx_rmsnorm_backward_workspace(rows, cols, need), "mx_rmsnorm_backward_workspace")
+    need = need.value
+    place, handle = _place(device, stream)
     with place:
         if dh is None:
-            dh = torch.empty((rows, cols), dtype=dy.dtype, device=dy.device)
-        g.dh, g.lddh = _rows_of(dh, "dh", dy)
-        dweight = torch.empty((cols,), dtype=torch.float32, device=dy.device)
-        g.dweight = dweight.data_ptr() if cols else None
-        work = torch.empty((need.value,), dtype=torch.uint8, device=dy.device)
-        st = lib.mx_rmsnorm_backward(ctypes.byref(g), work.data_ptr() if need.value else None,
-                                     need.value, handle)
+            dh = torch.empty((rows, cols), dtype=dy.dtype, device=device)
+            dp, lddh = dh.data_ptr() or None, cols
+        else:
+            dp, lddh = _rows_of(dh, "dh", dy)
+        dweight = torch.empty(cols, dtype=torch.float32, device=device)
+        work = torch.empty(need, dtype=torch.uint8, device=device)
+        g = NormGradDesc(yp, hp, rp, sp, wp, dp, dweight.data_ptr() or None, rows, cols, lddy, ldh,
+                         ldres, lddh, dtype, _row_dtype(weight, "weight"))
+        st = lib.mx_rmsnorm_backward(g, work.data_ptr() or None, need, handle)
     _check(st, "mx_rmsnorm_backward")
     return dh, dweight
 
@@ -726,19 +724,19 @@ def _norm_buffers(device, lib):
     import torch
     size = lib.mx_grad_workspace()
     return (torch.empty((), dtype=torch.float32, device=device),
-            torch.empty((size,), dtype=torch.uint8, device=device), size)
+            torch.empty(size, dtype=torch.uint8, device=device), size)
 
 
 def grad_norm(grads, stream=None):
     """Global 2-norm of a GradSet or of a list of gradients (see mx_grad_norm),
     a 0-dimensional fp32 CUDA tensor; with a GradSet nothing waits for the GPU."""
-    lib = load_library()
+    lib = _lib or load_library()
     grads, device = _grads_and_device(grads)
     place, handle = _place(device, stream)
     with place:
         s = _as_set(grads)
         norm, work, size = _norm_buffers(device, lib)
-        st = lib.mx_grad_norm(ctypes.byref(s.desc), norm.data_ptr(), work.data_ptr(), size, handle)
+        st = lib.mx_grad_norm(s.desc, norm.data_ptr(), work.data_ptr(), size, handle)
     _check(st, "mx_grad_norm")
     return norm
 
@@ -748,7 +746,7 @@ def clip_grad_norm(grads, max_norm: float, out=None, stream=None):
     2-norm, which is returned as grad_norm returns it (see mx_grad_clip). In
     place, or into `out`: tensors of the same shapes and types. Both may be
     GradSets, made once, or lists."""
-    lib = load_library()
+    lib = _lib or load_library()
     grads, device = _grads_and_device(grads)
     if out is not None:
         out, there = _grads_and_device(out)
@@ -759,7 +757,7 @@ def clip_grad_norm(grads, max_norm: float, out=None, stream=None):
         s = _as_set(grads)
         o = s if out is None else _as_set(out)
         norm, work, size = _norm_buffers(device, lib)
-        st = lib.mx_grad_clip(ctypes.byref(s.desc), ctypes.byref(o.desc), max_norm,
+        st = lib.mx_grad_clip(s.desc, o.desc, max_norm,
                               norm.data_ptr(), work.data_ptr(), size, handle)
     _check(st, "mx_grad_clip")
     return norm
