@@ -67,16 +67,19 @@ __device__ __forceinline__ float rstd_of(double sum, double inv_n, double eps) {
 }
 
 // ---------------------------------------------------------------------------
-// h and rstd of every row: a workgroup per row.
+// h and rstd of every row: a workgroup per row. ONCE: x and the residual are
+// kept out of the Infinity cache, so that h is still there when the pieces
+// below read it.
 // ---------------------------------------------------------------------------
-template <int F32>
+template <int F32, bool ONCE>
 __global__ __launch_bounds__(256) void norm_rows_kernel(NormArgs a) {
   const int64_t r = blockIdx.x;
+  auto read = [](const void *p, int64_t i) { return ONCE ? load8_once<F32>(p, i) : load8<F32>(p, i); };
   double acc = 0.0;
   for (int64_t c = threadIdx.x * 8; c < a.cols; c += 256 * 8) {
-    Row8<F32> v = load8<F32>(a.x, r * a.ldx + c);
+    Row8<F32> v = read(a.x, r * a.ldx + c);
     if (a.residual) {
-      v = add_rows<F32>(v, load8<F32>(a.residual, r * a.ldr + c));
+      v = add_rows<F32>(v, read(a.residual, r * a.ldr + c));
       store8<F32>(a.h, r * a.ldh + c, v);
     }
     float f[8];
@@ -89,6 +92,84 @@ __global__ __launch_bounds__(256) void norm_rows_kernel(NormArgs a) {
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = acc;
   __syncthreads();
   if (threadIdx.x == 0) a.rstd[r] = rstd_of(part[0] + part[1] + part[2] + part[3], a.inv_cols, a.eps);
+}
+
+// The block of y of row r at K = 32 kb of the axis-1 operand, rotated (random
+// signs: mask) and rounded; returns its scale code. The stochastic rounding
+// index is L = r * cols + 32 kb + i (cols % 32 == 0).
+template <int ROT, int RND, int FMT, int kWords>
+__device__ __forceinline__ uint32_t encode_row_block(const NormArgs &a, float (&y)[32], int64_t r,
+                                                     int64_t kb, uint32_t mask,
+                                                     uint32_t (&out)[kWords]) {
+  if (ROT == MX_K_ROT_RAND_SIGN) apply_sign_mask(y, mask);
+  rotate_block<ROT>(y);
+  const uint64_t q0 = (uint64_t)(r * a.cols + (kb << 5)) >> 2;
+  U4 w{0u, 0u, 0u, 0u};
+  auto u24_of = [&](int i) -> uint32_t {
+    if ((i & 3) == 0) w = sr_words(q0 + (uint64_t)(i >> 2), a.seed1_lo, a.seed1_hi);
+    return pick_word(w, (uint32_t)(i & 3)) >> 8;
+  };
+  return quantize_block<RotKind<ROT>::value, RND, FMT>(y, out, u24_of);
+}
+
+// The block of y of column c at rows R0 .. R0 + 31 of the axis-0 operand, as
+// above. With stochastic rounding the four lanes of a quad must hold four
+// columns c % 4 == 0 .. 3: element (R0 + i, c) draws word c % 4 of the call at
+// ((R0 + i) cols + c - c % 4) / 4, so each lane makes the calls of every fourth
+// row and a 4 x 4 transpose hands each its column's words.
+template <int ROT, int RND, int FMT, int kWords>
+__device__ __forceinline__ uint32_t encode_col_block(const NormArgs &a, float (&y)[32], int64_t R0,
+                                                     int64_t c, uint32_t mask,
+                                                     uint32_t (&out)[kWords]) {
+  if (ROT == MX_K_ROT_RAND_SIGN) apply_sign_mask(y, mask);
+  rotate_block<ROT>(y);
+  if constexpr (RND == MX_K_ROUND_SR) {
+    float m1, m2;
+    const uint32_t s = block_scale<RotKind<ROT>::value>(y, m1, m2);
+    const uint32_t q = (uint32_t)(c & 3);
+    const uint64_t lq0 = (uint64_t)R0 * (uint64_t)a.cols + (uint64_t)(c & ~(int64_t)3);
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) out[j] = 0u;
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      const U4 w = sr_words((lq0 + (uint64_t)(i + (int)q) * (uint64_t)a.cols) >> 2, a.seed0_lo,
+                            a.seed0_hi);
+      const uint32_t own = pick_word(w, q);
+      const uint32_t g1 =
+          (uint32_t)__builtin_amdgcn_update_dpp(0, (int)pick_word(w, q ^ 1u), 0xB1, 0xF, 0xF, false);
+      const uint32_t g2 =
+          (uint32_t)__builtin_amdgcn_update_dpp(0, (int)pick_word(w, q ^ 2u), 0x4E, 0xF, 0xF, false);
+      const uint32_t g3 =
+          (uint32_t)__builtin_amdgcn_update_dpp(0, (int)pick_word(w, q ^ 3u), 0x1B, 0xF, 0xF, false);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t d = (uint32_t)r ^ q;             // row i + r came from lane q ^ d
+        uint32_t u = own;
+        u = d == 1u ? g1 : u;
+        u = d == 2u ? g2 : u;
+        u = d == 3u ? g3 : u;
+        const uint32_t t = f_bits(__fmul_rn(__fmul_rn(y[i + r], m1), m2));
+        out[(i + r) >> 3] |= (e2m1_sr_mag(t & 0x7FFFFFFFu, u >> 8) | ((t >> 28) & 8u))
+                             << (4 * ((i + r) & 7));
+      }
+    }
+    if (s == 0xFFu) {
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) out[j] = 0u;
+    }
+    return s;
+  } else {
+    auto u24_of = [](int) -> uint32_t { return 0u; };   // nearest rounding draws nothing
+    return quantize_block<RotKind<ROT>::value, RND, FMT>(y, out, u24_of);
+  }
+}
+
+// A block's codes at p: 16 bytes, or E4M3's two 16-element chunks.
+template <int kWords>
+__device__ __forceinline__ void store_codes(uint8_t *p, const uint32_t (&out)[kWords]) {
+  *reinterpret_cast<uint4 *>(p) = make_uint4(out[0], out[1], out[2], out[3]);
+  if constexpr (kWords == 8)
+    *reinterpret_cast<uint4 *>(p + 256) = make_uint4(out[4], out[5], out[6], out[7]);
 }
 
 // ---------------------------------------------------------------------------
@@ -161,7 +242,8 @@ __global__ __launch_bounds__(MAXW * 64, 4) void norm_axis1_kernel(NormArgs a) {
   __shared__ __attribute__((aligned(16))) float stage[MAXW][kRows * kUnitCols];
   __shared__ uint8_t signs[ROT == MX_K_ROT_RAND_SIGN ? MAXW : 1][kUnitCols / 4];
   __shared__ double part[MAXW][kRows];
-  const int waves = blockDim.x >> 6, wv = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int waves = blockDim.x >> 6, lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t mnp = (a.rows + 255) & ~(int64_t)255;
   const uint32_t nblocks = (uint32_t)((a.cols + 127) >> 7) * 4;      // padding included
   const uint32_t nunits = (nblocks + kUnitBlocks - 1) / kUnitBlocks;
@@ -175,10 +257,8 @@ __global__ __launch_bounds__(MAXW * 64, 4) void norm_axis1_kernel(NormArgs a) {
   const uint32_t scales_row = (m >> 8) * 1024u + ((m >> 6) & 3) * 256u + (m & 15) * 4u + ((m >> 4) & 3);
   const uint32_t panels = (uint32_t)(mnp >> 8);
   auto put = [&](uint32_t kb, const uint32_t(&out)[kWords], uint32_t s) {
-    uint8_t *p = a.codes1 + (codes_row + (kb >> 2) * (kWords * 256u) + (kb & 3) * (kWords * 64u));
-    *reinterpret_cast<uint4 *>(p) = make_uint4(out[0], out[1], out[2], out[3]);
-    if constexpr (FMT == kFmtE4M3)      // the block's second 16-element chunk
-      *reinterpret_cast<uint4 *>(p + 256) = make_uint4(out[4], out[5], out[6], out[7]);
+    store_codes(a.codes1 + (codes_row + (kb >> 2) * (kWords * 256u) + (kb & 3) * (kWords * 64u)),
+                out);
     a.scales1[scales_row + (kb >> 2) * panels * 1024u + (kb & 3) * 64u] = (uint8_t)s;
   };
   if (r0 >= a.rows) {                                   // padding: zero codes, scale code 0
@@ -274,22 +354,12 @@ __global__ __launch_bounds__(MAXW * 64, 4) void norm_axis1_kernel(NormArgs a) {
       y[4 * j + 2] = f.z;
       y[4 * j + 3] = f.w;
     }
-    if (ROT == MX_K_ROT_RAND_SIGN) {
-      uint32_t mask = 0u;
+    uint32_t mask = 0u;
+    if (ROT == MX_K_ROT_RAND_SIGN)
 #pragma unroll
       for (int j = 0; j < 8; ++j) mask |= (uint32_t)sg[eb * 8 + j] << (4 * j);
-      apply_sign_mask(y, mask);
-    }
-    rotate_block<ROT>(y);
-    // stochastic rounding index L = r * cols + kb * 32 + i (cols % 32 == 0)
-    const uint64_t q0 = (uint64_t)((r0 + er) * a.cols + ((int64_t)kb << 5)) >> 2;
-    U4 words{0u, 0u, 0u, 0u};
-    auto u24_of = [&](int i) -> uint32_t {
-      if ((i & 3) == 0) words = sr_words(q0 + (uint64_t)(i >> 2), a.seed1_lo, a.seed1_hi);
-      return pick_word(words, (uint32_t)(i & 3)) >> 8;
-    };
     uint32_t out[kWords];
-    uint32_t s = quantize_block<RotKind<ROT>::value, RND, FMT>(y, out, u24_of);
+    uint32_t s = encode_row_block<ROT, RND, FMT>(a, y, r0 + er, kb, mask, out);
     if (r0 + er >= a.rows || ((int64_t)kb << 5) >= a.cols) {   // padding
 #pragma unroll
       for (int j = 0; j < kWords; ++j) out[j] = 0u;
@@ -313,11 +383,10 @@ __global__ __launch_bounds__(MAXW * 64, 4) void norm_axis1_kernel(NormArgs a) {
 // 0..127 encode its 128 row blocks and threads 128..255 its 128 column blocks.
 // ---------------------------------------------------------------------------
 template <int F32, int ROT, int RND, int FMT>
-__global__ __launch_bounds__(256) void norm_dual_kernel(NormArgs a, int64_t gx) {
+__global__ __launch_bounds__(256) void norm_dual_kernel(NormArgs a) {
   __shared__ __attribute__((aligned(16))) float st[32 * 132];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int64_t bx = (int64_t)blockIdx.x % gx, by = (int64_t)blockIdx.x / gx;
-  const int64_t C0 = bx * 128, R0 = by * 32;
+  const int64_t C0 = (int64_t)blockIdx.x * 128, R0 = (int64_t)blockIdx.y * 32;
   const int64_t nsl1 = (a.cols + 127) >> 7;   // axis-1 operand: MN = rows, K = cols
   const int64_t nsl0 = (a.rows + 127) >> 7;   // axis-0 operand: MN = cols, K = rows
   const int64_t mnp1 = (a.rows + 255) & ~(int64_t)255, mnp0 = (a.cols + 255) & ~(int64_t)255;
@@ -357,7 +426,6 @@ __global__ __launch_bounds__(256) void norm_dual_kernel(NormArgs a, int64_t gx) 
 #pragma unroll
   for (int j = 0; j < kWords; ++j) out[j] = 0u;
   uint32_t s = 0u;                                        // padding: zero codes, scale code 0
-  U4 w{0u, 0u, 0u, 0u};
   if (tid < 128) {
     // axis 1: row R0 + rr (< mnp1), 32-block kb along the columns
     const int rr = tid & 31, b = tid >> 5;
@@ -382,23 +450,10 @@ __global__ __launch_bounds__(256) void norm_dual_kernel(NormArgs a, int64_t gx) 
         y[4 * j + 2] = f.z;
         y[4 * j + 3] = f.w;
       }
-      if (ROT == MX_K_ROT_RAND_SIGN) apply_sign_mask(y, mask);
-      rotate_block<ROT>(y);
-      const uint64_t q0 = (uint64_t)(r * a.cols + (kb << 5)) >> 2;   // L % 4 == 0
-      auto u24_of = [&](int i) -> uint32_t {
-        if ((i & 3) == 0) w = sr_words(q0 + (uint64_t)(i >> 2), a.seed1_lo, a.seed1_hi);
-        return pick_word(w, (uint32_t)(i & 3)) >> 8;
-      };
-      s = quantize_block<RotKind<ROT>::value, RND, FMT>(y, out, u24_of);
+      s = encode_row_block<ROT, RND, FMT>(a, y, r, kb, mask, out);
     }
-    if constexpr (FMT == kFmtE4M3) {
-      uint8_t *p = a.codes1 + code_offset_e4m3(r, kb, nsl1);
-      *reinterpret_cast<uint4 *>(p) = make_uint4(out[0], out[1], out[2], out[3]);
-      *reinterpret_cast<uint4 *>(p + 256) = make_uint4(out[4], out[5], out[6], out[7]);
-    } else {
-      *reinterpret_cast<uint4 *>(a.codes1 + code_offset(r, kb, nsl1)) =
-          make_uint4(out[0], out[1], out[2], out[3]);
-    }
+    store_codes(a.codes1 + (FMT == kFmtE4M3 ? code_offset_e4m3(r, kb, nsl1)
+                                            : code_offset(r, kb, nsl1)), out);
     a.scales1[scale_offset(r, kb, mnp1)] = (uint8_t)s;
   } else {
     // axis 0: column C0 + cc (< mnp0), 32-block R0 / 32 along the rows
@@ -412,23 +467,10 @@ __global__ __launch_bounds__(256) void norm_dual_kernel(NormArgs a, int64_t gx) 
     if (rows_live && c < a.cols) {
 #pragma unroll
       for (int j = 0; j < 32; ++j) y[j] = st[j * 132 + cc];
-      if (ROT == MX_K_ROT_RAND_SIGN) apply_sign_mask(y, mask);
-      rotate_block<ROT>(y);
-      // element (R0 + i, c) has L = (R0 + i) cols + c
-      auto u24_of = [&](int i) -> uint32_t {
-        const uint64_t L = (uint64_t)((R0 + i) * a.cols + c);
-        return pick_word(sr_words(L >> 2, a.seed0_lo, a.seed0_hi), (uint32_t)(L & 3)) >> 8;
-      };
-      s = quantize_block<RotKind<ROT>::value, RND, FMT>(y, out, u24_of);
+      s = encode_col_block<ROT, RND, FMT>(a, y, R0, c, mask, out);
     }
-    if constexpr (FMT == kFmtE4M3) {
-      uint8_t *p = a.codes0 + code_offset_e4m3(c, kb, nsl0);
-      *reinterpret_cast<uint4 *>(p) = make_uint4(out[0], out[1], out[2], out[3]);
-      *reinterpret_cast<uint4 *>(p + 256) = make_uint4(out[4], out[5], out[6], out[7]);
-    } else {
-      *reinterpret_cast<uint4 *>(a.codes0 + code_offset(c, kb, nsl0)) =
-          make_uint4(out[0], out[1], out[2], out[3]);
-    }
+    store_codes(a.codes0 + (FMT == kFmtE4M3 ? code_offset_e4m3(c, kb, nsl0)
+                                            : code_offset(c, kb, nsl0)), out);
     a.scales0[scale_offset(c, kb, mnp0)] = (uint8_t)s;
   }
 }
@@ -443,15 +485,23 @@ hipError_t launch_norm(const NormArgs &a, hipStream_t stream) {
       return launch(norm_axis1_kernel<F32, ROT, RND, FMT, 8>, grid, dim3(waves * 64), 0, stream, a);
     return launch(norm_axis1_kernel<F32, ROT, RND, FMT, 16>, grid, dim3(waves * 64), 0, stream, a);
   }
-  const hipError_t e =
-      launch(norm_rows_kernel<F32>, dim3((unsigned)a.rows), dim3(256), 0, stream, a);
+  // Once x, the residual and h together fill three quarters of the 256 MB
+  // Infinity cache, the first two make way for h: 16384 x 4096 133 -> 112 us,
+  // 8192 x 4096 61.6 -> 60.1 us; with less they may be in it from what wrote
+  // them (16384 x 1024: 37.7 us, made to go 39.5 us). Without a residual h is
+  // x and stays.
+  const bool once = a.residual != nullptr &&
+                    a.rows * a.cols * (F32 ? 12 : 6) >= (int64_t)192 << 20;
+  const dim3 rows((unsigned)a.rows);
+  const hipError_t e = once ? launch(norm_rows_kernel<F32, true>, rows, dim3(256), 0, stream, a)
+                            : launch(norm_rows_kernel<F32, false>, rows, dim3(256), 0, stream, a);
   if (e != hipSuccess) return e;
   // columns up to the axis-0 operand's padded MN extent, rows up to the axis-1
   // operand's (each covers the other operand's K extent)
   const int64_t gx = ((a.cols + 255) & ~(int64_t)255) / 128;
   const int64_t gy = mnp / 32;
-  return launch(norm_dual_kernel<F32, ROT, RND, FMT>, dim3((unsigned)(gx * gy)), dim3(256), 0,
-                stream, a, gx);
+  return launch(norm_dual_kernel<F32, ROT, RND, FMT>, dim3((unsigned)gx, (unsigned)gy), dim3(256),
+                0, stream, a);
 }
 
 template <int ROT, int RND, int FMT>

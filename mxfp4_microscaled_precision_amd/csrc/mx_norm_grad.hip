@@ -38,9 +38,11 @@ __device__ __forceinline__ float group_sum(float v, float *part, int waves) {
 
 // V units of eight columns per thread cover a row in one go; wider rows take
 // norm_grad_wide_kernel. The next row's loads are in flight while the
-// workgroup adds up this one's products.
-template <int F32, int V>
+// workgroup adds up this one's products. ONCE: they are kept out of the
+// caches.
+template <int F32, int V, bool ONCE>
 __global__ __launch_bounds__(1024) void norm_grad_kernel(NormGradArgs a) {
+  auto take = [](const void *p, int64_t i) { return ONCE ? load8_once<F32>(p, i) : load8<F32>(p, i); };
   __shared__ float part[2][16];
   const int waves = blockDim.x >> 6;
   const float inv_n = 1.0f / (float)a.cols;
@@ -62,9 +64,9 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(NormGradArgs a) {
     rs = a.rstd[r];
 #pragma unroll
     for (int u = 0; u < V; ++u) {
-      h[u] = load8_once<F32>(a.h, r * a.ldh + col[u]);
-      dy[u] = load8_once<F32>(a.dy, r * a.lddy + col[u]);
-      if (a.dres) res[u] = load8_once<F32>(a.dres, r * a.ldres + col[u]);
+      h[u] = take(a.h, r * a.ldh + col[u]);
+      dy[u] = take(a.dy, r * a.lddy + col[u]);
+      if (a.dres) res[u] = take(a.dres, r * a.ldres + col[u]);
     }
   };
   int flip = 0;
@@ -183,7 +185,11 @@ __global__ __launch_bounds__(1024) void norm_grad_sum_kernel(const float *partia
 // One unit of eight columns per thread up to 8192 columns, two of bf16 rows up
 // to 16384 (2048 x 12288: 53 us, in two passes 81 us); fp32 rows would spill
 // there (198 us against 120 us) and take the two passes.
-template <int F32>
+// Rows that fill three quarters of the 256 MB Infinity cache are read past it
+// (16384 x 4096 bf16: 92 us, else 105 us; 2048 x 12288: 53 us, else 56 us);
+// smaller ones may be in it from what wrote them (4096 x 1024: 14.0 us, past
+// it 15.1 us).
+template <int F32, bool ONCE>
 hipError_t launch_grad(const NormGradArgs &a, hipStream_t stream) {
   const int64_t units = a.cols / 8;
   const int threads = (int)std::min<int64_t>(1024, (units + 63) / 64 * 64);
@@ -191,9 +197,9 @@ hipError_t launch_grad(const NormGradArgs &a, hipStream_t stream) {
   hipError_t e = hipSuccess;                           // without rows the sum writes zeros
   if (a.rows > 0) {
     if (units <= threads)
-      e = launch(norm_grad_kernel<F32, 1>, grid, dim3(threads), 0, stream, a);
+      e = launch(norm_grad_kernel<F32, 1, ONCE>, grid, dim3(threads), 0, stream, a);
     else if (!F32 && units <= 2 * threads)
-      e = launch(norm_grad_kernel<0, 2>, grid, dim3(threads), 0, stream, a);
+      e = launch(norm_grad_kernel<0, 2, ONCE>, grid, dim3(threads), 0, stream, a);
     else
       e = launch(norm_grad_wide_kernel<F32>, grid, dim3(threads), 0, stream, a);
   }
@@ -205,7 +211,10 @@ hipError_t launch_grad(const NormGradArgs &a, hipStream_t stream) {
 }  // namespace
 
 hipError_t norm_grad_launch(const NormGradArgs &a, hipStream_t stream) {
-  return a.f32 ? launch_grad<1>(a, stream) : launch_grad<0>(a, stream);
+  const bool once =
+      a.rows * a.cols * (a.f32 ? 4 : 2) * (a.dres != nullptr ? 4 : 3) >= (int64_t)192 << 20;
+  if (a.f32) return once ? launch_grad<1, true>(a, stream) : launch_grad<1, false>(a, stream);
+  return once ? launch_grad<0, true>(a, stream) : launch_grad<0, false>(a, stream);
 }
 
 }  // namespace mx

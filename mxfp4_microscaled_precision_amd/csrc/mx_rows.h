@@ -17,8 +17,8 @@ struct Row8 {
   row_u32x4 w[F32 ? 2 : 1];
 };
 
-template <int F32>
-__device__ __forceinline__ Row8<F32> load8(const void *base, int64_t i) {
+template <int F32, typename I>
+__device__ __forceinline__ Row8<F32> load8(const void *base, I i) {
   Row8<F32> r;
   const row_u32x4 *p = reinterpret_cast<const row_u32x4 *>(
       static_cast<const uint8_t *>(base) + i * (F32 ? 4 : 2));
@@ -28,8 +28,8 @@ __device__ __forceinline__ Row8<F32> load8(const void *base, int64_t i) {
 }
 
 // The same for data that is read once: kept out of the way of what is reused.
-template <int F32>
-__device__ __forceinline__ Row8<F32> load8_once(const void *base, int64_t i) {
+template <int F32, typename I>
+__device__ __forceinline__ Row8<F32> load8_once(const void *base, I i) {
   Row8<F32> r;
   const row_u32x4 *p = reinterpret_cast<const row_u32x4 *>(
       static_cast<const uint8_t *>(base) + i * (F32 ? 4 : 2));
@@ -38,8 +38,8 @@ __device__ __forceinline__ Row8<F32> load8_once(const void *base, int64_t i) {
   return r;
 }
 
-template <int F32>
-__device__ __forceinline__ void store8(void *base, int64_t i, const Row8<F32> &r) {
+template <int F32, typename I>
+__device__ __forceinline__ void store8(void *base, I i, const Row8<F32> &r) {
   row_u32x4 *p = reinterpret_cast<row_u32x4 *>(static_cast<uint8_t *>(base) + i * (F32 ? 4 : 2));
 #pragma unroll
   for (int k = 0; k < (F32 ? 2 : 1); ++k) p[k] = r.w[k];
