@@ -11,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG_DIR, "csrc")
@@ -45,11 +46,11 @@ def hipcc() -> str:
 
 def build(verbose: bool = False, extra_flags=None) -> str:
     """Compile every source and link libmxfp4.so next to this file."""
-    objs = []
     build_dir = os.path.join(PKG_DIR, "_build")
     os.makedirs(build_dir, exist_ok=True)
     flags = list(HIP_FLAGS) + list(extra_flags or [])
-    for src in SOURCES:
+
+    def compile_one(src: str) -> str:
         path = os.path.join(CSRC, src)
         obj = os.path.join(build_dir, os.path.splitext(src)[0] + ".o")
         lang = ["-x", "hip"]
@@ -61,7 +62,10 @@ def build(verbose: bool = False, extra_flags=None) -> str:
             raise RuntimeError(f"hipcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         if verbose and r.stderr.strip():
             print(r.stderr, file=sys.stderr)
-        objs.append(obj)
+        return obj
+
+    with ThreadPoolExecutor(max(1, min(8, len(os.sched_getaffinity(0))))) as pool:
+        objs = list(pool.map(compile_one, SOURCES))
     tmp = LIB_PATH + ".tmp"
     cmd = [hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -20,6 +20,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "mx_device.h"
 #include "mx_encode.h"
@@ -74,12 +75,11 @@ __device__ __forceinline__ float rstd_of(double sum, double inv_n, double eps) {
 template <int F32, bool ONCE>
 __global__ __launch_bounds__(256) void norm_rows_kernel(NormArgs a) {
   const int64_t r = blockIdx.x;
-  auto read = [](const void *p, int64_t i) { return ONCE ? load8_once<F32>(p, i) : load8<F32>(p, i); };
   double acc = 0.0;
   for (int64_t c = threadIdx.x * 8; c < a.cols; c += 256 * 8) {
-    Row8<F32> v = read(a.x, r * a.ldx + c);
+    Row8<F32> v = load8_if<F32, ONCE>(a.x, r * a.ldx + c);
     if (a.residual) {
-      v = add_rows<F32>(v, read(a.residual, r * a.ldr + c));
+      v = add_rows<F32>(v, load8_if<F32, ONCE>(a.residual, r * a.ldr + c));
       store8<F32>(a.h, r * a.ldh + c, v);
     }
     float f[8];
@@ -164,12 +164,19 @@ __device__ __forceinline__ uint32_t encode_col_block(const NormArgs &a, float (&
   }
 }
 
-// A block's codes at p: 16 bytes, or E4M3's two 16-element chunks.
-template <int kWords>
+// A block's codes at p: 16 bytes, or E4M3's two 16-element chunks. ONCE: past
+// the caches.
+template <bool ONCE, int kWords>
 __device__ __forceinline__ void store_codes(uint8_t *p, const uint32_t (&out)[kWords]) {
-  *reinterpret_cast<uint4 *>(p) = make_uint4(out[0], out[1], out[2], out[3]);
-  if constexpr (kWords == 8)
-    *reinterpret_cast<uint4 *>(p + 256) = make_uint4(out[4], out[5], out[6], out[7]);
+#pragma unroll
+  for (int i = 0; i < kWords / 4; ++i) {
+    const row_u32x4 v = {out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]};
+    row_u32x4 *q = reinterpret_cast<row_u32x4 *>(p + 256 * i);
+    if constexpr (ONCE)
+      __builtin_nontemporal_store(v, q);
+    else
+      *q = v;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -236,7 +243,7 @@ __device__ __forceinline__ void widen_weight(const Row8<1> &r, int f32, float (&
   }
 }
 
-template <int F32, int ROT, int RND, int FMT, int MAXW>
+template <int F32, int ROT, int RND, int FMT, bool ONCE, int MAXW>
 __global__ __launch_bounds__(MAXW * 64, 4) void norm_axis1_kernel(NormArgs a) {
   constexpr int kWords = FMT == kFmtE4M3 ? 8 : 4;
   __shared__ __attribute__((aligned(16))) float stage[MAXW][kRows * kUnitCols];
@@ -257,7 +264,7 @@ __global__ __launch_bounds__(MAXW * 64, 4) void norm_axis1_kernel(NormArgs a) {
   const uint32_t scales_row = (m >> 8) * 1024u + ((m >> 6) & 3) * 256u + (m & 15) * 4u + ((m >> 4) & 3);
   const uint32_t panels = (uint32_t)(mnp >> 8);
   auto put = [&](uint32_t kb, const uint32_t(&out)[kWords], uint32_t s) {
-    store_codes(a.codes1 + (codes_row + (kb >> 2) * (kWords * 256u) + (kb & 3) * (kWords * 64u)),
+    store_codes<false>(a.codes1 + (codes_row + (kb >> 2) * (kWords * 256u) + (kb & 3) * (kWords * 64u)),
                 out);
     a.scales1[scales_row + (kb >> 2) * panels * 1024u + (kb & 3) * 64u] = (uint8_t)s;
   };
@@ -273,20 +280,28 @@ __global__ __launch_bounds__(MAXW * 64, 4) void norm_axis1_kernel(NormArgs a) {
   // last row and not written; columns past the last are not read, and the
   // blocks there are padding.
   double acc[4] = {0.0, 0.0, 0.0, 0.0};
-  auto read_unit = [&](uint32_t u, Row8<F32>(&v)[4]) {
+  // held (a std::bool_constant): h is not read again here and is written past
+  // the caches
+  auto read_unit = [&](uint32_t u, Row8<F32>(&v)[4], auto held) {
     const int64_t k = (int64_t)u * kUnitCols + lane * 8;
     if (k >= a.cols) return;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = load8<F32>(a.x, min(r0 + j, a.rows - 1) * a.ldx + k);
+    for (int j = 0; j < 4; ++j)
+      v[j] = load8_if<F32, ONCE>(a.x, min(r0 + j, a.rows - 1) * a.ldx + k);
     if (a.residual) {
       Row8<F32> t[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        t[j] = load8<F32>(a.residual, min(r0 + j, a.rows - 1) * a.ldr + k);
+        t[j] = load8_if<F32, ONCE>(a.residual, min(r0 + j, a.rows - 1) * a.ldr + k);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         v[j] = add_rows<F32>(v[j], t[j]);
-        if (r0 + j < a.rows) store8<F32>(a.h, (r0 + j) * a.ldh + k, v[j]);
+        if (r0 + j < a.rows) {
+          if constexpr (decltype(held)::value)
+            store8_once<F32>(a.h, (r0 + j) * a.ldh + k, v[j]);
+          else
+            store8<F32>(a.h, (r0 + j) * a.ldh + k, v[j]);
+        }
       }
     }
 #pragma unroll
@@ -299,10 +314,10 @@ __global__ __launch_bounds__(MAXW * 64, 4) void norm_axis1_kernel(NormArgs a) {
   auto column = [&](uint32_t u) { return min((int64_t)u * kUnitCols + lane * 8, a.cols - 8); };
   Row8<F32> held[4];
   const Row8<1> w_held = load_weight_raw(a.weight, a.wf32, column(wv));
-  if (wv < (int)nunits) read_unit(wv, held);
+  if (wv < (int)nunits) read_unit(wv, held, std::true_type{});
   for (uint32_t u = wv + waves; u < nunits; u += waves) {
     Row8<F32> v[4];
-    read_unit(u, v);
+    read_unit(u, v, std::false_type{});
   }
 
   // row sums over the waves; every wave works out rstd of row l % 4 in lane l
@@ -382,7 +397,7 @@ __global__ __launch_bounds__(MAXW * 64, 4) void norm_axis1_kernel(NormArgs a) {
 // rows x 128 columns in LDS (fp32, row stride 132 floats), then threads
 // 0..127 encode its 128 row blocks and threads 128..255 its 128 column blocks.
 // ---------------------------------------------------------------------------
-template <int F32, int ROT, int RND, int FMT>
+template <int F32, int ROT, int RND, int FMT, bool ONCE>
 __global__ __launch_bounds__(256) void norm_dual_kernel(NormArgs a) {
   __shared__ __attribute__((aligned(16))) float st[32 * 132];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -452,7 +467,7 @@ __global__ __launch_bounds__(256) void norm_dual_kernel(NormArgs a) {
       }
       s = encode_row_block<ROT, RND, FMT>(a, y, r, kb, mask, out);
     }
-    store_codes(a.codes1 + (FMT == kFmtE4M3 ? code_offset_e4m3(r, kb, nsl1)
+    store_codes<ONCE>(a.codes1 + (FMT == kFmtE4M3 ? code_offset_e4m3(r, kb, nsl1)
                                             : code_offset(r, kb, nsl1)), out);
     a.scales1[scale_offset(r, kb, mnp1)] = (uint8_t)s;
   } else {
@@ -469,44 +484,50 @@ __global__ __launch_bounds__(256) void norm_dual_kernel(NormArgs a) {
       for (int j = 0; j < 32; ++j) y[j] = st[j * 132 + cc];
       s = encode_col_block<ROT, RND, FMT>(a, y, R0, c, mask, out);
     }
-    store_codes(a.codes0 + (FMT == kFmtE4M3 ? code_offset_e4m3(c, kb, nsl0)
+    store_codes<ONCE>(a.codes0 + (FMT == kFmtE4M3 ? code_offset_e4m3(c, kb, nsl0)
                                             : code_offset(c, kb, nsl0)), out);
     a.scales0[scale_offset(c, kb, mnp0)] = (uint8_t)s;
   }
 }
 
-template <int F32, int ROT, int RND, int FMT>
+template <int F32, int ROT, int RND, int FMT, bool ONCE>
 hipError_t launch_norm(const NormArgs &a, hipStream_t stream) {
   const int64_t mnp = (a.rows + 255) & ~(int64_t)255;
   if (a.codes0 == nullptr) {
     const int waves = (int)std::min<int64_t>(16, (a.cols + kUnitCols - 1) / kUnitCols);
-    const dim3 grid((unsigned)(mnp / kRows));
-    if (waves <= 8)
-      return launch(norm_axis1_kernel<F32, ROT, RND, FMT, 8>, grid, dim3(waves * 64), 0, stream, a);
-    return launch(norm_axis1_kernel<F32, ROT, RND, FMT, 16>, grid, dim3(waves * 64), 0, stream, a);
+    const dim3 grid((unsigned)(mnp / kRows)), block(waves * 64);
+    return waves <= 8
+               ? launch(norm_axis1_kernel<F32, ROT, RND, FMT, ONCE, 8>, grid, block, 0, stream, a)
+               : launch(norm_axis1_kernel<F32, ROT, RND, FMT, ONCE, 16>, grid, block, 0, stream, a);
   }
-  // Once x, the residual and h together fill three quarters of the 256 MB
-  // Infinity cache, the first two make way for h: 16384 x 4096 133 -> 112 us,
-  // 8192 x 4096 61.6 -> 60.1 us; with less they may be in it from what wrote
-  // them (16384 x 1024: 37.7 us, made to go 39.5 us). Without a residual h is
-  // x and stays.
-  const bool once = a.residual != nullptr &&
-                    a.rows * a.cols * (F32 ? 12 : 6) >= (int64_t)192 << 20;
+  // without a residual h is x and stays
   const dim3 rows((unsigned)a.rows);
-  const hipError_t e = once ? launch(norm_rows_kernel<F32, true>, rows, dim3(256), 0, stream, a)
-                            : launch(norm_rows_kernel<F32, false>, rows, dim3(256), 0, stream, a);
+  const hipError_t e = ONCE && a.residual
+                           ? launch(norm_rows_kernel<F32, true>, rows, dim3(256), 0, stream, a)
+                           : launch(norm_rows_kernel<F32, false>, rows, dim3(256), 0, stream, a);
   if (e != hipSuccess) return e;
   // columns up to the axis-0 operand's padded MN extent, rows up to the axis-1
   // operand's (each covers the other operand's K extent)
   const int64_t gx = ((a.cols + 255) & ~(int64_t)255) / 128;
-  const int64_t gy = mnp / 32;
-  return launch(norm_dual_kernel<F32, ROT, RND, FMT>, dim3((unsigned)gx, (unsigned)gy), dim3(256),
-                0, stream, a);
+  return launch(norm_dual_kernel<F32, ROT, RND, FMT, ONCE>,
+                dim3((unsigned)gx, (unsigned)(mnp / 32)), dim3(256), 0, stream, a);
 }
 
 template <int ROT, int RND, int FMT>
 hipError_t launch_norm_type(const NormArgs &a, hipStream_t stream) {
-  return a.f32 ? launch_norm<1, ROT, RND, FMT>(a, stream) : launch_norm<0, ROT, RND, FMT>(a, stream);
+  // Once x, the residual and h together fill three quarters of the 256 MB
+  // Infinity cache, x and the residual are read around it, so that h is still
+  // there for the second launch of the two-operand pass, and that launch's
+  // codes are written around it (16384 x 4096: 129.5 us, with both 115.5 us). In
+  // one pass (8192 x 4096) 49.8 -> 46.9 us. With less the rows may be there
+  // from what wrote them (16384 x 1024, two operands: 37.7 us, read around the
+  // cache 39.5 us), and the codes for the products that read them.
+  const bool once = a.rows * a.cols * (a.f32 ? 4 : 2) * (a.residual ? 3 : 1) >= (int64_t)192 << 20;
+  if (a.f32)
+    return once ? launch_norm<1, ROT, RND, FMT, true>(a, stream)
+                : launch_norm<1, ROT, RND, FMT, false>(a, stream);
+  return once ? launch_norm<0, ROT, RND, FMT, true>(a, stream)
+              : launch_norm<0, ROT, RND, FMT, false>(a, stream);
 }
 
 }  // namespace

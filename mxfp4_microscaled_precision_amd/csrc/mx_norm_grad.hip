@@ -42,7 +42,6 @@ __device__ __forceinline__ float group_sum(float v, float *part, int waves) {
 // caches.
 template <int F32, int V, bool ONCE>
 __global__ __launch_bounds__(1024) void norm_grad_kernel(NormGradArgs a) {
-  auto take = [](const void *p, int64_t i) { return ONCE ? load8_once<F32>(p, i) : load8<F32>(p, i); };
   __shared__ float part[2][16];
   const int waves = blockDim.x >> 6;
   const float inv_n = 1.0f / (float)a.cols;
@@ -64,9 +63,9 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(NormGradArgs a) {
     rs = a.rstd[r];
 #pragma unroll
     for (int u = 0; u < V; ++u) {
-      h[u] = take(a.h, r * a.ldh + col[u]);
-      dy[u] = take(a.dy, r * a.lddy + col[u]);
-      if (a.dres) res[u] = take(a.dres, r * a.ldres + col[u]);
+      h[u] = load8_if<F32, ONCE>(a.h, r * a.ldh + col[u]);
+      dy[u] = load8_if<F32, ONCE>(a.dy, r * a.lddy + col[u]);
+      if (a.dres) res[u] = load8_if<F32, ONCE>(a.dres, r * a.ldres + col[u]);
     }
   };
   int flip = 0;

@@ -38,11 +38,29 @@ __device__ __forceinline__ Row8<F32> load8_once(const void *base, I i) {
   return r;
 }
 
+// Either, chosen at compile time: the compiler makes one ordinary load or store
+// of the two sides of a branch.
+template <int F32, bool ONCE, typename I>
+__device__ __forceinline__ Row8<F32> load8_if(const void *base, I i) {
+  if constexpr (ONCE)
+    return load8_once<F32>(base, i);
+  else
+    return load8<F32>(base, i);
+}
+
 template <int F32, typename I>
 __device__ __forceinline__ void store8(void *base, I i, const Row8<F32> &r) {
   row_u32x4 *p = reinterpret_cast<row_u32x4 *>(static_cast<uint8_t *>(base) + i * (F32 ? 4 : 2));
 #pragma unroll
   for (int k = 0; k < (F32 ? 2 : 1); ++k) p[k] = r.w[k];
+}
+
+// For data that is not read again soon: the store does not displace what is.
+template <int F32, typename I>
+__device__ __forceinline__ void store8_once(void *base, I i, const Row8<F32> &r) {
+  row_u32x4 *p = reinterpret_cast<row_u32x4 *>(static_cast<uint8_t *>(base) + i * (F32 ? 4 : 2));
+#pragma unroll
+  for (int k = 0; k < (F32 ? 2 : 1); ++k) __builtin_nontemporal_store(r.w[k], p + k);
 }
 
 template <int F32>
