@@ -20,7 +20,7 @@ LIB_NAME = "libmxfp4.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 SOURCES = ["mx_quant.hip", "mx_gemm.hip", "mx_gemm_e4m3.hip", "mx_dequant.hip", "mx_norm.hip",
-           "mx_norm_grad.hip", "mx_clip.hip", "mx_api.cpp"]
+           "mx_norm_dual.hip", "mx_norm_grad.hip", "mx_clip.hip", "mx_api.cpp"]
 
 # -ffp-contract=off: the rotation's adds and multiplies must round one by one.
 # -packed-fp32-ops off: packed fp32 VALU forms are not used by this library.

@@ -124,6 +124,8 @@ struct NormArgs {
 };
 
 hipError_t norm_launch(const NormArgs &a, hipStream_t stream);
+// The two-operand case (codes0 != nullptr) of the above.
+hipError_t norm_dual_launch(const NormArgs &a, hipStream_t stream);
 
 // Gradient of the norm.
 struct NormGradArgs {
