@@ -23,6 +23,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional, Tuple
 
@@ -567,6 +568,21 @@ def _vector(t, name: str, n: int, device):
     return t.data_ptr() if n else None
 
 
+@functools.lru_cache(maxsize=256)
+def _norm_sizes(fmt: int, rows: int, cols: int, dual: bool) -> Tuple[int, ...]:
+    """Bytes of codes1, scales1 (and codes0, scales0), a function of the shape."""
+    sizes = quantize_fp8_sizes if fmt else quantize_sizes
+    return sizes(rows, cols, 1) + (sizes(rows, cols, 0) if dual else ())
+
+
+@functools.lru_cache(maxsize=256)
+def _backward_workspace(rows: int, cols: int) -> int:
+    need = ctypes.c_size_t()
+    _check(load_library().mx_rmsnorm_backward_workspace(rows, cols, need),
+           "mx_rmsnorm_backward_workspace")
+    return need.value
+
+
 class RMSNormQuantized(NamedTuple):
     """What rmsnorm_quantize returns: the axis-1 and axis-0 operands of y (q0 is
     None without dual), the residual stream h and rstd per row."""
@@ -596,8 +612,7 @@ def rmsnorm_quantize(x, weight, residual=None, eps: float = 1e-5, format: str = 
     wp = _vector(weight, "weight", cols, device)
     rp, ldr = (None, 0) if residual is None else _rows_of(residual, "residual", x)
     fmt = FORMATS[format]
-    sizes = quantize_fp8_sizes if fmt else quantize_sizes
-    size = sizes(rows, cols, 1) + (sizes(rows, cols, 0) if dual else ())
+    size = _norm_sizes(fmt, rows, cols, bool(dual))
     place, handle = _place(device, stream)
     with place:
         if residual is None:
@@ -643,9 +658,7 @@ def rmsnorm_backward(dy, h, rstd, weight, dres=None, dh=None, stream=None):
         raise ValueError("rstd must be float32")
     sp = _vector(rstd, "rstd", rows, device)
     wp = _vector(weight, "weight", cols, device)
-    need = ctypes.c_size_t()
-    _check(lib.mx_rmsnorm_backward_workspace(rows, cols, need), "mx_rmsnorm_backward_workspace")
-    need = need.value
+    need = _backward_workspace(rows, cols)
     place, handle = _place(device, stream)
     with place:
         if dh is None:
