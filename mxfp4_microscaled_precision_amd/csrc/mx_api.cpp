@@ -591,8 +591,9 @@ mx_status grad_layout(int32_t count, const mx_grad *grads, GradLayout *l) {
 mx_status check_set(const mx_grad_set *s) {
   if (s == nullptr) return MX_ERR_NULL;
   if (s->count < 0 || s->chunks < 0) return MX_ERR_ARG;
+  if (s->count > 0 && s->grads == nullptr) return MX_ERR_NULL;
   if (s->chunks > 0) {
-    if (s->grads == nullptr || s->host_table == nullptr || s->table == nullptr) return MX_ERR_NULL;
+    if (s->host_table == nullptr || s->table == nullptr) return MX_ERR_NULL;
     if (!aligned(s->table, 8)) return MX_ERR_ALIGN;
   }
   return MX_OK;

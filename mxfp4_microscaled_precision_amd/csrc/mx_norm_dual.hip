@@ -47,10 +47,11 @@ __global__ __launch_bounds__(256) void norm_rows_kernel(NormArgs a) {
 // 0..127 encode its 128 row blocks and threads 128..255 its 128 column blocks.
 // ---------------------------------------------------------------------------
 template <int F32, int ROT, int RND, int FMT, bool ONCE>
-__global__ __launch_bounds__(256) void norm_dual_kernel(NormArgs a) {
+__global__ __launch_bounds__(256) void norm_dual_kernel(NormArgs a, uint32_t gx) {
   __shared__ __attribute__((aligned(16))) float st[32 * 132];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int64_t C0 = (int64_t)blockIdx.x * 128, R0 = (int64_t)blockIdx.y * 32;
+  const uint32_t by = blockIdx.x / gx, bx = blockIdx.x - by * gx;
+  const int64_t C0 = (int64_t)bx * 128, R0 = (int64_t)by * 32;
   const int64_t nsl1 = (a.cols + 127) >> 7;   // axis-1 operand: MN = rows, K = cols
   const int64_t nsl0 = (a.rows + 127) >> 7;   // axis-0 operand: MN = cols, K = rows
   const int64_t mnp1 = (a.rows + 255) & ~(int64_t)255, mnp0 = (a.cols + 255) & ~(int64_t)255;
@@ -158,8 +159,8 @@ struct DualLaunch {
     // axis-1 operand's (each covers the other operand's K extent)
     const int64_t gx = ((a.cols + 255) & ~(int64_t)255) / 128;
     const int64_t gy = ((a.rows + 255) & ~(int64_t)255) / 32;
-    return launch(norm_dual_kernel<F32, ROT, RND, FMT, ONCE>, dim3((unsigned)gx, (unsigned)gy),
-                  dim3(256), 0, stream, a);
+    return launch(norm_dual_kernel<F32, ROT, RND, FMT, ONCE>, dim3((unsigned)(gx * gy)), dim3(256), 0,
+                  stream, a, (uint32_t)gx);
   }
   static hipError_t run(const NormArgs &a, hipStream_t stream) {
     const bool once = norm_once(a);

@@ -169,6 +169,10 @@ def test_grad_norm_and_clip_refuse(lib):
     for bad in (-1.0, float("nan")):
         assert lib.mx_grad_clip(ref(s), None, bad, P, P, W, None) == -4
     assert lib.mx_grad_clip(ref(s), None, 1.0, None, P, W, None) == -1
+    bare = mx.GradSetDesc()
+    bare.count = 3                                              # tensors, but no array of them
+    assert lib.mx_grad_norm(ref(bare), P, P, W, None) == -1
+    assert lib.mx_grad_clip(ref(s), ref(bare), 1.0, P, P, W, None) == -1
     far = P + (1 << 20)
     for want, other in [
             (-5, [(far, 2, 8, 8, 0)]), (-5, [(far, 2, 8, 8, 0), (far + 64, 2, 8, 8, 0)]),

@@ -156,6 +156,27 @@ def test_extreme_magnitudes(mx):
     assert torch.isinf(mx.grad_norm([big]))
 
 
+@pytest.mark.parametrize("bf16", [True, False])
+def test_offsets_beyond_32_bits(mx, bf16):
+    """A tensor of more than 4 GiB, without gaps and with: only a few elements,
+    the first and last among them, are not zero."""
+    import torch
+    n = (1 << 32) // (2 if bf16 else 4) + 4099
+    at = torch.tensor([0, 1, n // 2, n - 4100, n - 2, n - 1], device="cuda")
+    v = torch.tensor([3.0, -4.0, 12.0, 1.0, 2.0, -2.0], device="cuda")
+    g = torch.zeros(n, dtype=torch.bfloat16 if bf16 else torch.float32, device="cuda")
+    g[at] = v.to(g.dtype)
+    norm = float(np.sqrt(178.0))
+    _norm_close(mx.clip_grad_norm([g], 1.0), norm)
+    _close(g[at], (v.double().cpu().numpy()) / (norm + 1e-6), bf16)
+    assert int(torch.count_nonzero(g)) == 6
+    g[at] = v.to(g.dtype)
+    wide = g[:n // 64 * 64].view(-1, 64)[:, :33]            # the column slice's elements only
+    keep = (at % 64 < 33) & (at < n // 64 * 64)
+    norm = float(v[keep].double().square().sum().sqrt())
+    _norm_close(mx.grad_norm([wide]), norm)
+
+
 def test_nonfinite_and_limits(mx):
     import torch
     for bad in (float("nan"), float("inf"), float("-inf")):

@@ -139,30 +139,74 @@ def test_in_place(mx, cols, bf16):
 
 
 def test_large_rows_sampled(mx):
-    """The block's tokens and width: the first and last rows, and rows around
-    every panel border of the sample, against the oracle; the rest through
-    dequantize of both orientations agreeing with each other on scale-free
-    facts is left to the smaller shapes."""
+    """The block's tokens and width, where the rows outgrow the caches: the
+    first, middle and last row blocks against the oracle."""
     import torch
     rows, cols = 16384, 4096
     gen = torch.Generator(device="cuda").manual_seed(4)
     x = torch.randn(rows, cols, generator=gen, device="cuda").bfloat16()
     r = torch.randn(rows, cols, generator=gen, device="cuda").bfloat16()
     w = 1 + 0.1 * torch.randn(cols, generator=gen, device="cuda")
-    got = mx.rmsnorm_quantize(x, w, r, dual=True, format="fp8_e4m3")
-    pick = np.r_[0:32, 8160:8224, 16352:16384]
-    h, rstd, y = oracle.rmsnorm_ref(host(x[pick]), host(w), host(r[pick]), EPS, True)
-    assert np.array_equal(host(got.h[pick]), h)
-    assert np.array_equal(host(got.rstd[pick]), rstd)
+    _sampled(mx, x, w, r, np.r_[0:32, 8160:8224, 16352:16384], True)
+    _sampled(mx, x, w, r, np.r_[0:32, 8160:8224, 16352:16384], False)
+
+
+def _sampled(mx, x, w, r, pick, dual, fmt="fp8_e4m3", bf16=True):
+    """Rows `pick` (whole 32-row blocks with dual) against the oracle."""
+    rows, cols = x.shape
+    got = mx.rmsnorm_quantize(x, w, r, dual=dual, format=fmt)
+    h, rstd, y = oracle.rmsnorm_ref(host(x[pick]), host(w), host(r[pick]), EPS, bf16)
+    assert np.array_equal(host(got.h[pick]), h) and np.array_equal(host(got.rstd[pick]), rstd)
+    q = oracle.quantize_values_ref(y, 1, fmt=fmt)
     codes, scales = got.q1.codes.cpu().numpy(), got.q1.scales.cpu().numpy()
-    q = oracle.quantize_values_ref(y, 1, fmt="fp8_e4m3")
     assert np.array_equal(oracle.untile_codes_fp8(codes, rows, cols)[pick], q.codes)
     assert np.array_equal(oracle.untile_scales(scales, rows, cols)[pick], q.scales)
-    q = oracle.quantize_values_ref(y, 0, fmt="fp8_e4m3")          # whole 32-row blocks
-    codes, scales = got.q0.codes.cpu().numpy(), got.q0.scales.cpu().numpy()
-    blocks = pick.reshape(-1, 32)[:, 0] // 32
-    assert np.array_equal(oracle.untile_codes_fp8(codes, cols, rows)[:, pick], q.codes)
-    assert np.array_equal(oracle.untile_scales(scales, cols, rows)[:, blocks], q.scales)
+    if dual:
+        q = oracle.quantize_values_ref(y, 0, fmt=fmt)
+        codes, scales = got.q0.codes.cpu().numpy(), got.q0.scales.cpu().numpy()
+        blocks = pick.reshape(-1, 32)[:, 0] // 32
+        assert np.array_equal(oracle.untile_codes_fp8(codes, cols, rows)[:, pick], q.codes)
+        assert np.array_equal(oracle.untile_scales(scales, cols, rows)[:, blocks], q.scales)
+
+
+def test_large_f32_rows_sampled(mx):
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x, r = (torch.randn(4096, 4096, generator=gen, device="cuda") for _ in range(2))
+    w = (1 + 0.1 * torch.randn(4096, generator=gen, device="cuda")).bfloat16()
+    for dual in (False, True):
+        _sampled(mx, x, w, r, np.r_[0:32, 2016:2080, 4064:4096], dual, bf16=False)
+
+
+def test_many_rows(mx):
+    """More 32-row pieces than a grid's second extent may count (65535)."""
+    import torch
+    rows, cols = 65536 * 32 + 64, 32
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    x, r = (torch.randn(rows, cols, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    w = 1 + 0.1 * torch.randn(cols, generator=gen, device="cuda")
+    pick = np.r_[0:32, 65535 * 32:65537 * 32, rows - 32:rows]
+    _sampled(mx, x, w, r, pick, True)
+
+
+@pytest.mark.parametrize("dual", [False, True])
+def test_offsets_beyond_32_bits(mx, dual):
+    """Rows that lie more than 4 GiB after the first."""
+    import torch
+    rows, cols, ld = 64, 256, 1 << 26
+    big = torch.empty((rows * ld,), dtype=torch.bfloat16, device="cuda").view(rows, ld)
+    x = big[:, 64:64 + cols]
+    r, h = big[:, 1024:1024 + cols], big[:, 4096:4096 + cols]
+    rng = np.random.default_rng(15)
+    xv, rv, w = (values(rng, s, True) for s in ((rows, cols), (rows, cols), (cols,)))
+    x.copy_(dev(xv, True))
+    r.copy_(dev(rv, True))
+    got = mx.rmsnorm_quantize(x, dev(w, True), r, h=h, dual=dual, format="fp8_e4m3")
+    href, rstd, y = oracle.rmsnorm_ref(xv, w, rv, EPS, True)
+    assert np.array_equal(host(h), href) and np.array_equal(host(got.rstd), rstd)
+    check_operand(got.q1, y, 1, "hadamard", "rne", 0, "fp8_e4m3", "far rows")
+    if dual:
+        check_operand(got.q0, y, 0, "hadamard", "rne", 0, "fp8_e4m3", "far rows")
 
 
 def test_operand_feeds_linear(mx):

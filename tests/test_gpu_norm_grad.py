@@ -58,7 +58,7 @@ def _check(got, dy, h, rstd, w, d, bf16):
 
 @pytest.mark.parametrize("rows,cols", [(1, 8), (1, 4096), (3, 40), (32, 512), (777, 1056),
                                        (1100, 328), (2048, 4096), (65, 8192), (40, 14336),
-                                       (9, 16416), (700, 40008), (5000, 64)])
+                                       (9, 16416), (700, 40008), (5000, 64), (6000, 4096)])
 @pytest.mark.parametrize("bf16", [True, False])
 def test_against_oracle(mx, rows, cols, bf16):
     for dres, wbf16 in ((True, bf16), (False, not bf16)):
@@ -115,6 +115,19 @@ def test_strided_and_in_place(mx, cols):
                                       dh=(a, b)[over])
             assert got[0] is (a, b)[over]
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_offsets_beyond_32_bits(mx):
+    import torch
+    rows, cols, ld = 64, 256, 1 << 26
+    big = torch.empty((rows * ld,), dtype=torch.bfloat16, device="cuda").view(rows, ld)
+    parts = [big[:, k * 1024:k * 1024 + cols] for k in range(4)]
+    dy, h, rstd, w, d = _inputs(rows, cols, True, True, True)
+    for p, v in zip(parts, (dy, h, d)):
+        p.copy_(dev(v, True))
+    got = mx.rmsnorm_backward(parts[0], parts[1], dev(rstd, False), dev(w, True), parts[2],
+                              dh=parts[3])
+    _check(got, dy, h, rstd, w, d, True)
 
 
 def test_deterministic_and_nonfinite(mx):
