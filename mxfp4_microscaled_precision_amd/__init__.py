@@ -530,28 +530,36 @@ def _place(device, stream):
     return torch.cuda.stream(stream), stream.cuda_stream
 
 
+_ROW_DTYPES = {}
+
+
 def _row_dtype(t, name: str) -> int:
-    import torch
-    dtype = t.dtype
-    if dtype is torch.bfloat16:
-        return 1
-    if dtype is torch.float32:
-        return 0
-    raise ValueError(f"{name} must be bfloat16 or float32")
+    if not _ROW_DTYPES:
+        import torch
+        _ROW_DTYPES.update({torch.float32: OUT_DTYPES["f32"], torch.bfloat16: OUT_DTYPES["bf16"]})
+    dtype = _ROW_DTYPES.get(t.dtype)
+    if dtype is None:
+        raise ValueError(f"{name} must be bfloat16 or float32")
+    return dtype
 
 
-def _rows_of(t, name: str, like=None) -> Tuple[Optional[int], int]:
-    """(address, leading dimension) of a 2-D CUDA matrix with unit column
-    stride, of like's type, shape and device."""
+def _first_rows(t, name: str) -> Tuple[int, int]:
+    """(rows, cols) of the 2-D CUDA matrix that sets a call's type and shape."""
     shape = t.shape
     if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA (HIP) tensor; there is no CPU path")
-    if like is not None and (t.dtype is not like.dtype or shape != like.shape
-                             or t.device != like.device):
+    return shape
+
+
+def _rows_of(t, name: str, rows: int, cols: int, dtype, device) -> Tuple[Optional[int], int]:
+    """(address, leading dimension) of a matrix of the given shape, type and
+    device with unit column stride."""
+    shape = t.shape
+    if (len(shape) != 2 or shape[0] != rows or shape[1] != cols or t.dtype is not dtype
+            or t.device != device):
         raise ValueError(f"{name} must have the type, shape and device of the other rows")
-    rows, cols = shape
     if rows == 0 or cols == 0:
         return None, (cols + 7) // 8 * 8
     ld, unit = t.stride()
@@ -561,7 +569,8 @@ def _rows_of(t, name: str, like=None) -> Tuple[Optional[int], int]:
 
 
 def _vector(t, name: str, n: int, device):
-    if t.dim() != 1 or t.shape[0] != n or t.device != device:
+    shape = t.shape
+    if len(shape) != 1 or shape[0] != n or t.device != device:
         raise ValueError(f"{name} must be a 1-D tensor of {n} elements on the rows' device")
     if n > 1 and t.stride(0) != 1:
         raise ValueError(f"{name} must be contiguous")
@@ -606,11 +615,12 @@ def rmsnorm_quantize(x, weight, residual=None, eps: float = 1e-5, format: str = 
     """
     import torch
     lib = _lib or load_library()
-    xp, ldx = _rows_of(x, "x")
-    dtype, device = _row_dtype(x, "x"), x.device
-    rows, cols = x.shape
+    rows, cols = _first_rows(x, "x")
+    kind, dtype, device = x.dtype, _row_dtype(x, "x"), x.device
+    xp, ldx = _rows_of(x, "x", rows, cols, kind, device)
     wp = _vector(weight, "weight", cols, device)
-    rp, ldr = (None, 0) if residual is None else _rows_of(residual, "residual", x)
+    rp, ldr = ((None, 0) if residual is None
+               else _rows_of(residual, "residual", rows, cols, kind, device))
     fmt = FORMATS[format]
     size = _norm_sizes(fmt, rows, cols, bool(dual))
     place, handle = _place(device, stream)
@@ -620,10 +630,10 @@ def rmsnorm_quantize(x, weight, residual=None, eps: float = 1e-5, format: str = 
                 raise ValueError("without a residual h is x itself")
             h, hp, ldh = x, None, 0
         elif h is None:
-            h = torch.empty((rows, cols), dtype=x.dtype, device=device)
+            h = torch.empty((rows, cols), dtype=kind, device=device)
             hp, ldh = h.data_ptr(), cols
         else:
-            hp, ldh = _rows_of(h, "h", x)
+            hp, ldh = _rows_of(h, "h", rows, cols, kind, device)
         rstd = torch.empty(rows, dtype=torch.float32, device=device)
         buf = [torch.empty(b, dtype=torch.uint8, device=device) for b in size]
         ptr = [b.data_ptr() or None for b in buf] + [None, None]
@@ -649,11 +659,11 @@ def rmsnorm_backward(dy, h, rstd, weight, dres=None, dh=None, stream=None):
     residual; it may be written over dy or dres. dweight is fp32."""
     import torch
     lib = _lib or load_library()
-    yp, lddy = _rows_of(dy, "dy")
-    dtype, device = _row_dtype(dy, "dy"), dy.device
-    rows, cols = dy.shape
-    hp, ldh = _rows_of(h, "h", dy)
-    rp, ldres = (None, 0) if dres is None else _rows_of(dres, "dres", dy)
+    rows, cols = _first_rows(dy, "dy")
+    kind, dtype, device = dy.dtype, _row_dtype(dy, "dy"), dy.device
+    yp, lddy = _rows_of(dy, "dy", rows, cols, kind, device)
+    hp, ldh = _rows_of(h, "h", rows, cols, kind, device)
+    rp, ldres = (None, 0) if dres is None else _rows_of(dres, "dres", rows, cols, kind, device)
     if rstd.dtype is not torch.float32:
         raise ValueError("rstd must be float32")
     sp = _vector(rstd, "rstd", rows, device)
@@ -662,10 +672,10 @@ def rmsnorm_backward(dy, h, rstd, weight, dres=None, dh=None, stream=None):
     place, handle = _place(device, stream)
     with place:
         if dh is None:
-            dh = torch.empty((rows, cols), dtype=dy.dtype, device=device)
+            dh = torch.empty((rows, cols), dtype=kind, device=device)
             dp, lddh = dh.data_ptr() or None, cols
         else:
-            dp, lddh = _rows_of(dh, "dh", dy)
+            dp, lddh = _rows_of(dh, "dh", rows, cols, kind, device)
         dweight = torch.empty(cols, dtype=torch.float32, device=device)
         work = torch.empty(need, dtype=torch.uint8, device=device)
         g = NormGradDesc(yp, hp, rp, sp, wp, dp, dweight.data_ptr() or None, rows, cols, lddy, ldh,
