@@ -14,6 +14,9 @@
  * one E8M0 exponent, each element an E2M1 4-bit float (same page, section
  * "Was ist MXFP4?"), rounded to nearest-even or stochastically.
  *
+ * Around the linears stand the RMS norm of the residual stream into packed
+ * operands, its gradient, and clipping by the global gradient norm.
+ *
  * Conventions for every call:
  *  - All tensor pointers are DEVICE pointers (hipMalloc / torch CUDA memory)
  *    on the current HIP device. The caller allocates and owns every buffer;
