@@ -68,7 +68,10 @@ __device__ __forceinline__ void widen_weight(const Row8<1> &r, int f32, float (&
 
 // The block of y of row r at K = 32 kb of the axis-1 operand, rotated (random
 // signs: mask) and rounded; returns its scale code. The stochastic rounding
-// index is L = r * cols + 32 kb + i (cols % 32 == 0).
+// index is L = r * cols + 32 kb + i (cols % 32 == 0). quantize_block multiplies
+// once by c * 2^-e where the rule multiplies twice: for y of more bits than
+// bf16 the two agree unless a rotated value is subnormal in fp32 (below
+// 2^-126), where they may pick different neighbours of a tie.
 template <int ROT, int RND, int FMT, int kWords>
 __device__ __forceinline__ uint32_t encode_row_block(const NormArgs &a, float (&y)[32], int64_t r,
                                                      int64_t kb, uint32_t mask,
@@ -151,8 +154,9 @@ __device__ __forceinline__ void store_codes(uint8_t *p, const uint32_t (&out)[kW
   }
 }
 
-// Once x, the residual and h together fill three quarters of the 256 MB
-// Infinity cache they are read around it: see the two launchers.
+// Whether x, the residual and h together fill three quarters of the 256 MB
+// Infinity cache, and are then read around it: see the two launchers for both
+// sides' times.
 inline bool norm_once(const NormArgs &a) {
   return a.rows * a.cols * (a.f32 ? 4 : 2) * (a.residual ? 3 : 1) >= (int64_t)192 << 20;
 }
