@@ -611,7 +611,9 @@ def rmsnorm_quantize(x, weight, residual=None, eps: float = 1e-5, format: str = 
     weight: bf16 or fp32 [cols]. format, rotate, round and the seeds are those
     of quantize_dual / quantize_fp8; dual adds the axis-0 operand. h: where the
     stream is written, may be residual or x itself to update it in place; x is
-    returned as h where there is no residual.
+    returned as h where there is no residual. stream: a torch stream or a raw
+    handle to run on instead of the current one; the outputs are allocated for
+    it, and the inputs must be ready there.
     """
     import torch
     lib = _lib or load_library()
@@ -630,7 +632,8 @@ def rmsnorm_quantize(x, weight, residual=None, eps: float = 1e-5, format: str = 
                 raise ValueError("without a residual h is x itself")
             h, hp, ldh = x, None, 0
         elif h is None:
-            h = torch.empty((rows, cols), dtype=kind, device=device)
+            h = (torch.empty_like(x) if ldx == cols and rows > 1
+                 else torch.empty((rows, cols), dtype=kind, device=device))
             hp, ldh = h.data_ptr(), cols
         else:
             hp, ldh = _rows_of(h, "h", rows, cols, kind, device)
@@ -672,7 +675,8 @@ def rmsnorm_backward(dy, h, rstd, weight, dres=None, dh=None, stream=None):
     place, handle = _place(device, stream)
     with place:
         if dh is None:
-            dh = torch.empty((rows, cols), dtype=kind, device=device)
+            dh = (torch.empty_like(dy) if lddy == cols and rows > 1
+                  else torch.empty((rows, cols), dtype=kind, device=device))
             dp, lddh = dh.data_ptr() or None, cols
         else:
             dp, lddh = _rows_of(dh, "dh", rows, cols, kind, device)

@@ -141,7 +141,8 @@ struct NormGradArgs {
 
 // Workgroups of the gradient's row pass, one partial weight gradient each: 16
 // waves to a compute unit where that leaves each at least eight rows, up to 512
-// workgroups of them where there are fewer rows. A function of the shape alone, so
+// workgroups of them where there are fewer rows (2048 x 8192: 30.8 us with the
+// 256 that fit, 36.8 us with 512). A function of the shape alone, so
 // that the order of the sums is too.
 inline int norm_grad_groups(int64_t rows, int64_t cols) {
   const int64_t waves = cols >= 16 * 512 ? 16 : (cols + 511) / 512;

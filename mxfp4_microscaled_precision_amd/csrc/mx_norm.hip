@@ -231,7 +231,10 @@ __global__ __launch_bounds__(MAXW * 64, 4) void norm_axis1_kernel(NormArgs a) {
 }
 
 // Rows that outgrow the caches (norm_once) are read past them: 8192 x 4096
-// 49.8 -> 46.9 us; fewer may be there from what wrote them.
+// 49.8 -> 46.9 us; fewer may be there from what wrote them. Up to 4096 columns
+// a workgroup asks for the LDS of eight waves, so that two share a compute
+// unit (8192 x 4096 46.4 us, with sixteen waves' LDS 54.7 us); wider rows need
+// sixteen.
 template <int ROT, int RND, int FMT>
 struct Axis1Launch {
   template <int F32, bool ONCE>
