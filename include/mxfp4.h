@@ -436,7 +436,8 @@ typedef struct mx_norm_grad {
 } mx_norm_grad;
 
 /*
- * Bytes of the workspace of mx_rmsnorm_backward. Host-only.
+ * Bytes of the workspace of mx_rmsnorm_backward (0 for few rows: none is
+ * needed then). Host-only.
  * Errors: MX_ERR_NULL, MX_ERR_SHAPE, MX_ERR_UNSUPPORTED (extents above 2^31).
  */
 mx_status mx_rmsnorm_backward_workspace(int64_t rows, int64_t cols, size_t *bytes);

@@ -681,10 +681,10 @@ def rmsnorm_backward(dy, h, rstd, weight, dres=None, dh=None, stream=None):
         else:
             dp, lddh = _rows_of(dh, "dh", rows, cols, kind, device)
         dweight = torch.empty(cols, dtype=torch.float32, device=device)
-        work = torch.empty(need, dtype=torch.uint8, device=device)
+        work = torch.empty(need, dtype=torch.uint8, device=device) if need else None
         g = NormGradDesc(yp, hp, rp, sp, wp, dp, dweight.data_ptr() or None, rows, cols, lddy, ldh,
                          ldres, lddh, dtype, _row_dtype(weight, "weight"))
-        st = lib.mx_rmsnorm_backward(g, work.data_ptr() or None, need, handle)
+        st = lib.mx_rmsnorm_backward(g, work.data_ptr() if need else None, need, handle)
     _check(st, "mx_rmsnorm_backward")
     return dh, dweight
 

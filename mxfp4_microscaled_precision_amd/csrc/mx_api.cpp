@@ -491,7 +491,9 @@ mx_status mx_rmsnorm_backward_workspace(int64_t rows, int64_t cols, size_t *byte
   if (bytes == nullptr) return MX_ERR_NULL;
   if (rows < 0 || cols < 0) return MX_ERR_SHAPE;
   if (extents_too_large(rows, cols)) return MX_ERR_UNSUPPORTED;
-  *bytes = (size_t)mx::norm_grad_groups(rows, cols) * (size_t)cols * sizeof(float);
+  *bytes = mx::norm_grad_few(rows, cols)
+               ? 0
+               : (size_t)mx::norm_grad_groups(rows, cols) * (size_t)cols * sizeof(float);
   return MX_OK;
 }
 
@@ -508,7 +510,8 @@ mx_status mx_rmsnorm_backward(const mx_norm_grad *g, void *workspace, size_t wor
   if (g->dweight == nullptr) return MX_ERR_NULL;
   if (!aligned(g->dweight, 16)) return MX_ERR_ALIGN;
   if (rows > 0) {
-    if (g->rstd == nullptr || g->weight == nullptr || workspace == nullptr) return MX_ERR_NULL;
+    if (g->rstd == nullptr || g->weight == nullptr || (need > 0 && workspace == nullptr))
+      return MX_ERR_NULL;
     const void *m[4] = {g->dy, g->h, g->dh, g->dres};
     const int64_t ld[4] = {g->lddy, g->ldh, g->lddh, g->ldres};
     for (int i = 0; i < (g->dres != nullptr ? 4 : 3); ++i) {

@@ -11,7 +11,7 @@
 // A workgroup walks rows with a stride of the grid: a thread owns the same
 // columns of each, so the weight's gradient stays in its registers and one
 // partial row per workgroup reaches memory. A second launch adds the partial
-// rows in a fixed order (no atomics). Row sums and the partial rows are fp32,
+// rows in a fixed order (no atomics). A few rows take one launch. Row sums and the partial rows are fp32,
 // the sum over workgroups is fp64.
 //
 // 16384 x 4096 bf16 with dres: 85.4 us for 547 MB (6.4 TB/s: bound by HBM)
@@ -157,6 +157,64 @@ __global__ __launch_bounds__(1024) void norm_grad_wide_kernel(NormGradArgs a) {
   }
 }
 
+// Few rows in one launch: a workgroup of sixteen waves owns 512 columns. Each
+// works out the dot products of all rows by itself (wave w those of rows w and
+// w + 16), then dh of its columns, and adds the waves' parts of the weight's
+// gradient in LDS.
+
+template <int F32>
+__global__ __launch_bounds__(1024) void norm_grad_few_kernel(NormGradArgs a) {
+  __shared__ float dots[kFewRows];
+  __shared__ __attribute__((aligned(16))) float sums[16][512];
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const float inv_n = 1.0f / (float)a.cols;
+  for (int r = wv; r < a.rows; r += 16) {
+    const float rs = a.rstd[r];
+    float dot = 0.f;
+    for (int64_t c = lane * 8; c < a.cols; c += 512) {
+      float x[8], g[8], w[8];
+      widen8<F32>(load8<F32>(a.h, r * a.ldh + c), x);
+      widen8<F32>(load8<F32>(a.dy, r * a.lddy + c), g);
+      load_weight8(a.weight, a.wf32, c, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dot = __fmaf_rn(g[i] * w[i], x[i] * rs, dot);
+    }
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) dot += __shfl_xor(dot, m);
+    if (lane == 0) dots[r] = dot * inv_n;
+  }
+  __syncthreads();
+  const int64_t c = (int64_t)blockIdx.x * 512 + lane * 8;
+  float dw[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (c < a.cols) {
+    float w[8];
+    load_weight8(a.weight, a.wf32, c, w);
+    for (int r = wv; r < a.rows; r += 16) {
+      const float rs = a.rstd[r], m = dots[r];
+      float x[8], g[8], o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      widen8<F32>(load8<F32>(a.h, r * a.ldh + c), x);
+      widen8<F32>(load8<F32>(a.dy, r * a.lddy + c), g);
+      if (a.dres) widen8<F32>(load8<F32>(a.dres, r * a.ldres + c), o);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] *= rs;
+        dw[i] = __fmaf_rn(g[i], x[i], dw[i]);
+        o[i] = __fmaf_rn(__fmaf_rn(x[i], -m, g[i] * w[i]), rs, o[i]);
+      }
+      store8<F32>(a.dh, r * a.lddh + c, narrow8<F32>(o));
+    }
+  }
+  store8<1>(sums[wv], lane * 8, narrow8<1>(dw));
+  __syncthreads();
+  if (threadIdx.x >= 512) return;
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s += sums[i][threadIdx.x];
+  const int64_t col = (int64_t)blockIdx.x * 512 + threadIdx.x;
+  if (col < a.cols) a.dweight[col] = s;
+}
+
 // dweight[c] = sum of the partial rows, in 64 bits: 32 columns per workgroup,
 // 32 threads to a column, all of a thread's loads in flight together.
 __global__ __launch_bounds__(1024) void norm_grad_sum_kernel(const float *partial, int groups,
@@ -195,6 +253,9 @@ __global__ __launch_bounds__(1024) void norm_grad_sum_kernel(const float *partia
 // it 15.1 us).
 template <int F32, bool ONCE>
 hipError_t launch_grad(const NormGradArgs &a, hipStream_t stream) {
+  if (norm_grad_few(a.rows, a.cols))
+    return launch(norm_grad_few_kernel<F32>, dim3((unsigned)((a.cols + 511) / 512)), dim3(1024),
+                  0, stream, a);
   const int64_t units = a.cols / 8;
   const int threads = (int)std::min<int64_t>(1024, (units + 63) / 64 * 64);
   const dim3 grid((unsigned)norm_grad_groups(a.rows, a.cols));

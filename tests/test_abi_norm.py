@@ -69,12 +69,12 @@ def _back(lib, work=P, size=1 << 30, null=False, **f):
 @pytest.mark.parametrize("want,args", [
     (-1, dict(null=True)), (-4, dict(dtype=3)), (-4, dict(weight_dtype=2)),
     (-2, dict(rows=-1)), (-2, dict(cols=60)), (-2, dict(lddy=32)), (-2, dict(ldh=32)),
-    (-2, dict(ldres=32)), (-2, dict(lddh=32)), (-2, dict(lddh=128)), (-2, dict(size=64 * 64 * 4 - 1)),
+    (-2, dict(ldres=32)), (-2, dict(lddh=32)), (-2, dict(lddh=128)), (-2, dict(rows=4096, size=4095)),
     (-1, dict(dy=None)), (-1, dict(h=None)), (-1, dict(rstd=None)), (-1, dict(weight=None)),
-    (-1, dict(dh=None)), (-1, dict(dweight=None)), (-1, dict(work=None)),
+    (-1, dict(dh=None)), (-1, dict(dweight=None)), (-1, dict(rows=4096, work=None)),
     (-3, dict(dy=P + 8)), (-3, dict(h=P + 8)), (-3, dict(dres=P + 8)), (-3, dict(dh=P + 8)),
     (-3, dict(rstd=P + 2)), (-3, dict(weight=P + 8)), (-3, dict(dweight=P + 4)),
-    (-3, dict(work=P + 8)), (-3, dict(lddy=68)), (-3, dict(dtype=F32, ldh=66)),
+    (-3, dict(rows=4096, work=P + 8)), (-3, dict(lddy=68)), (-3, dict(dtype=F32, ldh=66)),
     (-6, dict(rows=(1 << 31) + 1)), (-6, dict(rows=1 << 20, ldh=1 << 60)),
 ])
 def test_rmsnorm_backward_refuses(lib, want, args):
@@ -84,7 +84,9 @@ def test_rmsnorm_backward_refuses(lib, want, args):
 def test_backward_workspace(lib):
     n = ctypes.c_size_t()
     assert lib.mx_rmsnorm_backward_workspace(7, 64, ctypes.byref(n)) == 0
-    assert 7 * 64 * 4 >= n.value > 0 and n.value % (64 * 4) == 0
+    assert n.value == 0                                 # few rows: one launch, no partial rows
+    assert lib.mx_rmsnorm_backward_workspace(700, 64, ctypes.byref(n)) == 0
+    assert 700 * 64 * 4 >= n.value > 0 and n.value % (64 * 4) == 0
     assert lib.mx_rmsnorm_backward_workspace(1 << 30, 64, ctypes.byref(n)) == 0
     assert n.value <= 4096 * 64 * 4                     # bounded, whatever the rows
     assert lib.mx_rmsnorm_backward_workspace(7, 64, None) == -1

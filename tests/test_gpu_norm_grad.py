@@ -56,7 +56,9 @@ def _check(got, dy, h, rstd, w, d, bf16):
     assert np.all(err <= limit), f"dweight: {(err / limit).max():.3g} of the bound"
 
 
-@pytest.mark.parametrize("rows,cols", [(1, 8), (1, 4096), (3, 40), (32, 512), (777, 1056),
+@pytest.mark.parametrize("rows,cols", [(1, 8), (1, 4096), (3, 40), (32, 512), (64, 1024),
+                                       (8, 4096), (9, 4096), (31, 1000), (32, 1024), (33, 512), (16, 2048),
+                                       (1, 4104), (2, 16), (777, 1056),
                                        (1100, 328), (2048, 4096), (65, 8192), (40, 14336),
                                        (9, 16416), (700, 40008), (5000, 64), (6000, 4096)])
 @pytest.mark.parametrize("bf16", [True, False])
