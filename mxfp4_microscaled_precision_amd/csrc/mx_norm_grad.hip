@@ -185,34 +185,37 @@ __global__ __launch_bounds__(1024) void norm_grad_few_kernel(NormGradArgs a) {
     if (lane == 0) dots[r] = dot * inv_n;
   }
   __syncthreads();
-  const int64_t c = (int64_t)blockIdx.x * 512 + lane * 8;
-  float dw[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (c < a.cols) {
-    float w[8];
-    load_weight8(a.weight, a.wf32, c, w);
-    for (int r = wv; r < a.rows; r += 16) {
-      const float rs = a.rstd[r], m = dots[r];
-      float x[8], g[8], o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      widen8<F32>(load8<F32>(a.h, r * a.ldh + c), x);
-      widen8<F32>(load8<F32>(a.dy, r * a.lddy + c), g);
-      if (a.dres) widen8<F32>(load8<F32>(a.dres, r * a.ldres + c), o);
+  for (int64_t c0 = (int64_t)blockIdx.x * 512; c0 < a.cols; c0 += (int64_t)gridDim.x * 512) {
+    const int64_t c = c0 + lane * 8;
+    float dw[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (c < a.cols) {
+      float w[8];
+      load_weight8(a.weight, a.wf32, c, w);
+      for (int r = wv; r < a.rows; r += 16) {
+        const float rs = a.rstd[r], m = dots[r];
+        float x[8], g[8], o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        widen8<F32>(load8<F32>(a.h, r * a.ldh + c), x);
+        widen8<F32>(load8<F32>(a.dy, r * a.lddy + c), g);
+        if (a.dres) widen8<F32>(load8<F32>(a.dres, r * a.ldres + c), o);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] *= rs;
-        dw[i] = __fmaf_rn(g[i], x[i], dw[i]);
-        o[i] = __fmaf_rn(__fmaf_rn(x[i], -m, g[i] * w[i]), rs, o[i]);
+        for (int i = 0; i < 8; ++i) {
+          x[i] *= rs;
+          dw[i] = __fmaf_rn(g[i], x[i], dw[i]);
+          o[i] = __fmaf_rn(__fmaf_rn(x[i], -m, g[i] * w[i]), rs, o[i]);
+        }
+        store8<F32>(a.dh, r * a.lddh + c, narrow8<F32>(o));
       }
-      store8<F32>(a.dh, r * a.lddh + c, narrow8<F32>(o));
     }
-  }
-  store8<1>(sums[wv], lane * 8, narrow8<1>(dw));
-  __syncthreads();
-  if (threadIdx.x >= 512) return;
-  float s = 0.f;
+    store8<1>(sums[wv], lane * 8, narrow8<1>(dw));
+    __syncthreads();
+    if (threadIdx.x < 512 && c0 + threadIdx.x < a.cols) {
+      float s = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) s += sums[i][threadIdx.x];
-  const int64_t col = (int64_t)blockIdx.x * 512 + threadIdx.x;
-  if (col < a.cols) a.dweight[col] = s;
+      for (int i = 0; i < 16; ++i) s += sums[i][threadIdx.x];
+      a.dweight[c0 + threadIdx.x] = s;
+    }
+    __syncthreads();                                    // sums is read
+  }
 }
 
 // dweight[c] = sum of the partial rows, in 64 bits: 32 columns per workgroup,
@@ -253,9 +256,12 @@ __global__ __launch_bounds__(1024) void norm_grad_sum_kernel(const float *partia
 // it 15.1 us).
 template <int F32, bool ONCE>
 hipError_t launch_grad(const NormGradArgs &a, hipStream_t stream) {
-  if (norm_grad_few(a.rows, a.cols))
-    return launch(norm_grad_few_kernel<F32>, dim3((unsigned)((a.cols + 511) / 512)), dim3(1024),
-                  0, stream, a);
+  if (norm_grad_few(a.rows, a.cols)) {
+    // every workgroup reads all of dy: where dh is written over it, one does
+    // all the columns, after its own reads
+    const unsigned groups = a.dh == a.dy ? 1u : (unsigned)((a.cols + 511) / 512);
+    return launch(norm_grad_few_kernel<F32>, dim3(groups), dim3(1024), 0, stream, a);
+  }
   const int64_t units = a.cols / 8;
   const int threads = (int)std::min<int64_t>(1024, (units + 63) / 64 * 64);
   const dim3 grid((unsigned)norm_grad_groups(a.rows, a.cols));

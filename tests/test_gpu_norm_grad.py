@@ -132,6 +132,24 @@ def test_offsets_beyond_32_bits(mx):
     _check(got, dy, h, rstd, w, d, True)
 
 
+@pytest.mark.parametrize("rows,cols", [(1, 4096), (8, 4096), (16, 2048), (32, 1024), (32, 512)])
+def test_few_rows_in_place(mx, rows, cols):
+    """Few rows take one launch, whose workgroups all read the whole of dy: over
+    dy, over dres and beside both give the same dh, and so does dweight."""
+    import torch
+    for bf16 in (True, False):
+        dy, h, rstd, w, d = _inputs(rows, cols, bf16, True, True)
+        rest = dev(h, bf16), dev(rstd, False), dev(w, True)
+        want = mx.rmsnorm_backward(dev(dy, bf16), *rest, dev(d, bf16))
+        for _ in range(20):
+            a, b = dev(dy, bf16), dev(d, bf16)
+            got = mx.rmsnorm_backward(a, *rest, b, dh=a)
+            assert got[0] is a and torch.equal(a, want[0]) and torch.equal(got[1], want[1])
+            a = dev(dy, bf16)
+            got = mx.rmsnorm_backward(a, *rest, b, dh=b)
+            assert got[0] is b and torch.equal(b, want[0]) and torch.equal(got[1], want[1])
+
+
 def test_deterministic_and_nonfinite(mx):
     import torch
     dy, h, rstd, w, d = _inputs(1500, 520, True, True, True)
