@@ -419,7 +419,7 @@ mx_status mx_rmsnorm_quantize(const mx_norm *n, int32_t format, int32_t block, i
  *             norm, or NULL for none.
  *  dh         device [rows, cols], lddh. Written. May be dy or dres itself
  *             (same pointer and leading dimension); must not overlap the
- *             inputs otherwise.
+ *             inputs otherwise (h itself is refused: MX_ERR_ARG).
  *  dweight    device fp32 [cols], 16-byte aligned. Written.
  *  dtype      of dy, h, dres and dh; weight_dtype of weight.
  * Alignment and leading dimensions as for mx_norm; rstd 4-byte aligned.

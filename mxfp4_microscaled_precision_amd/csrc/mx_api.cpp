@@ -518,6 +518,7 @@ mx_status mx_rmsnorm_backward(const mx_norm_grad *g, void *workspace, size_t wor
       st = check_rows(m[i], rows, cols, ld[i], g->dtype);
       if (st != MX_OK) return st;
     }
+    if (g->dh == g->h) return MX_ERR_ARG;
     if ((g->dh == g->dy && g->lddh != g->lddy) || (g->dh == g->dres && g->lddh != g->ldres) ||
         workspace_bytes < need)
       return MX_ERR_SHAPE;

@@ -60,7 +60,7 @@ def test_rmsnorm_quantize_empty_fills_descriptors(lib):
 
 
 def _back(lib, work=P, size=1 << 30, null=False, **f):
-    g = mx.NormGradDesc(P, P, P, P, P, P, P, 64, 64, 64, 64, 64, 64, BF16, F32)
+    g = mx.NormGradDesc(P, 2 * P, P, P, P, P, P, 64, 64, 64, 64, 64, 64, BF16, F32)
     for k, v in f.items():
         setattr(g, k, v)
     return lib.mx_rmsnorm_backward(None if null else ctypes.byref(g), work, size, None)
@@ -68,6 +68,7 @@ def _back(lib, work=P, size=1 << 30, null=False, **f):
 
 @pytest.mark.parametrize("want,args", [
     (-1, dict(null=True)), (-4, dict(dtype=3)), (-4, dict(weight_dtype=2)),
+    (-4, dict(h=P)),                                            # dh over h
     (-2, dict(rows=-1)), (-2, dict(cols=60)), (-2, dict(lddy=32)), (-2, dict(ldh=32)),
     (-2, dict(ldres=32)), (-2, dict(lddh=32)), (-2, dict(lddh=128)), (-2, dict(rows=4096, size=4095)),
     (-1, dict(dy=None)), (-1, dict(h=None)), (-1, dict(rstd=None)), (-1, dict(weight=None)),
