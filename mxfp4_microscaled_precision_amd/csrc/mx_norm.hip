@@ -136,15 +136,8 @@ __global__ __launch_bounds__(MAXW * 64, 4) void norm_axis1_kernel(NormArgs a) {
 #pragma unroll
     for (int n = 0; n < kParts; ++n) {
       const int64_t k = F32 ? part_col(u, n) : min(part_col(u, n), a.cols - kPartCols);
-      const row_u32x4 *q = reinterpret_cast<const row_u32x4 *>(
-          static_cast<const uint8_t *>(p) + (row0 + k) * (F32 ? 4 : 2));
       v.w[n] = row_u32x4{0u, 0u, 0u, 0u};
-      if (!F32 || k < a.cols) {
-        if constexpr (decltype(once)::value)
-          v.w[n] = __builtin_nontemporal_load(q);
-        else
-          v.w[n] = *q;
-      }
+      if (!F32 || k < a.cols) v.w[n] = load16<F32, decltype(once)::value>(p, row0 + k);
     }
     return v;
   };
@@ -167,12 +160,7 @@ __global__ __launch_bounds__(MAXW * 64, 4) void norm_axis1_kernel(NormArgs a) {
 #pragma unroll
           for (int n = 0; n < kParts; ++n) {
             if (F32 && part_col(u, n) >= a.cols) continue;
-            row_u32x4 *q = reinterpret_cast<row_u32x4 *>(
-                static_cast<uint8_t *>(a.h) + ((r0 + j) * a.ldh + part_col(u, n)) * (F32 ? 4 : 2));
-            if constexpr (decltype(held)::value)
-              __builtin_nontemporal_store(v[j].w[n], q);
-            else
-              *q = v[j].w[n];
+            store16<F32, decltype(held)::value>(a.h, (r0 + j) * a.ldh + part_col(u, n), v[j].w[n]);
           }
         }
       }

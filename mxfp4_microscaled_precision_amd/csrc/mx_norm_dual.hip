@@ -33,21 +33,12 @@ __global__ __launch_bounds__(256) void norm_rows_kernel(NormArgs a) {
   // (fp32), so that each access of a wave covers whole lines (both launches at
   // 8192 x 4096 fp32: 96.7 us, by 8 adjacent columns 108.2 us).
   constexpr int kParts = F32 ? 2 : 1, kPartCols = 8 / kParts;
-  auto at = [&](const void *p, int64_t i) {
-    return reinterpret_cast<row_u32x4 *>(
-        const_cast<uint8_t *>(static_cast<const uint8_t *>(p)) + i * (F32 ? 4 : 2));
-  };
   auto load = [&](const void *p, int64_t row0, const int64_t (&c)[kParts]) {
     Row8<F32> v;
 #pragma unroll
     for (int n = 0; n < kParts; ++n) {
       v.w[n] = row_u32x4{0u, 0u, 0u, 0u};
-      if (n == 0 || c[n] < a.cols) {
-        if constexpr (ONCE)
-          v.w[n] = __builtin_nontemporal_load(at(p, row0 + c[n]));
-        else
-          v.w[n] = *at(p, row0 + c[n]);
-      }
+      if (n == 0 || c[n] < a.cols) v.w[n] = load16<F32, ONCE>(p, row0 + c[n]);
     }
     return v;
   };
@@ -60,7 +51,7 @@ __global__ __launch_bounds__(256) void norm_rows_kernel(NormArgs a) {
       v = add_rows<F32>(v, load(a.residual, r * a.ldr, c));
 #pragma unroll
       for (int n = 0; n < kParts; ++n)
-        if (n == 0 || c[n] < a.cols) *at(a.h, r * a.ldh + c[n]) = v.w[n];
+        if (n == 0 || c[n] < a.cols) store16<F32, false>(a.h, r * a.ldh + c[n], v.w[n]);
     }
     float f[8];
     widen8<F32>(v, f);

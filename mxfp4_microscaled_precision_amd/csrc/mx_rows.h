@@ -27,25 +27,26 @@ __device__ __forceinline__ Row8<F32> load8(const void *base, I i) {
   return r;
 }
 
-// The same for data that is read once: kept out of the way of what is reused.
-template <int F32, typename I>
-__device__ __forceinline__ Row8<F32> load8_once(const void *base, I i) {
-  Row8<F32> r;
-  const row_u32x4 *p = reinterpret_cast<const row_u32x4 *>(
-      static_cast<const uint8_t *>(base) + i * (F32 ? 4 : 2));
-#pragma unroll
-  for (int k = 0; k < (F32 ? 2 : 1); ++k) r.w[k] = __builtin_nontemporal_load(p + k);
-  return r;
+// 16 bytes of a row from element i on. ONCE: they are not read again soon, so
+// the access does not displace what is. It is a template parameter because the
+// compiler merges the two sides of a branch and drops the hint.
+template <int F32, bool ONCE, typename I>
+__device__ __forceinline__ row_u32x4 load16(const void *base, I i) {
+  const row_u32x4 *p = reinterpret_cast<const row_u32x4 *>(static_cast<const uint8_t *>(base) +
+                                                           i * (F32 ? 4 : 2));
+  if constexpr (ONCE)
+    return __builtin_nontemporal_load(p);
+  else
+    return *p;
 }
 
-// Either, chosen at compile time: the compiler makes one ordinary load or store
-// of the two sides of a branch.
 template <int F32, bool ONCE, typename I>
-__device__ __forceinline__ Row8<F32> load8_if(const void *base, I i) {
+__device__ __forceinline__ void store16(void *base, I i, row_u32x4 v) {
+  row_u32x4 *p = reinterpret_cast<row_u32x4 *>(static_cast<uint8_t *>(base) + i * (F32 ? 4 : 2));
   if constexpr (ONCE)
-    return load8_once<F32>(base, i);
+    __builtin_nontemporal_store(v, p);
   else
-    return load8<F32>(base, i);
+    *p = v;
 }
 
 template <int F32, typename I>
@@ -53,14 +54,6 @@ __device__ __forceinline__ void store8(void *base, I i, const Row8<F32> &r) {
   row_u32x4 *p = reinterpret_cast<row_u32x4 *>(static_cast<uint8_t *>(base) + i * (F32 ? 4 : 2));
 #pragma unroll
   for (int k = 0; k < (F32 ? 2 : 1); ++k) p[k] = r.w[k];
-}
-
-// For data that is not read again soon: the store does not displace what is.
-template <int F32, typename I>
-__device__ __forceinline__ void store8_once(void *base, I i, const Row8<F32> &r) {
-  row_u32x4 *p = reinterpret_cast<row_u32x4 *>(static_cast<uint8_t *>(base) + i * (F32 ? 4 : 2));
-#pragma unroll
-  for (int k = 0; k < (F32 ? 2 : 1); ++k) __builtin_nontemporal_store(r.w[k], p + k);
 }
 
 template <int F32>
@@ -103,6 +96,23 @@ __device__ __forceinline__ void load_weight8(const void *w, int f32, int64_t i, 
     widen8<1>(load8<1>(w, i), v);
   else
     widen8<0>(load8<0>(w, i), v);
+}
+
+// Four of them.
+__device__ __forceinline__ void load_weight4(const void *w, int f32, int64_t i, float *v) {
+  if (f32) {
+    const float4 f = *reinterpret_cast<const float4 *>(static_cast<const float *>(w) + i);
+    v[0] = f.x;
+    v[1] = f.y;
+    v[2] = f.z;
+    v[3] = f.w;
+  } else {
+    const uint2 b = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(w) + i);
+    v[0] = __builtin_bit_cast(float, b.x << 16);
+    v[1] = __builtin_bit_cast(float, b.x & 0xFFFF0000u);
+    v[2] = __builtin_bit_cast(float, b.y << 16);
+    v[3] = __builtin_bit_cast(float, b.y & 0xFFFF0000u);
+  }
 }
 
 }  // namespace mx
