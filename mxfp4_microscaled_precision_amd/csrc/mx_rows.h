@@ -1,5 +1,6 @@
-// Row access shared by the norm and its gradient: eight consecutive elements
-// of a bf16 or fp32 row (16 or 32 bytes) as one unit, widened to fp32.
+// Row access shared by the norm and its gradient: eight elements of a bf16 or
+// fp32 row (16 or 32 bytes) as one unit, adjacent ones or two times four,
+// widened to fp32.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -11,7 +12,7 @@ namespace mx {
 
 typedef uint32_t row_u32x4 __attribute__((ext_vector_type(4)));
 
-// Eight elements as they lie in memory. F32: fp32 rows, else bf16.
+// Eight elements in their type, 16 bytes to a word. F32: fp32 rows, else bf16.
 template <int F32>
 struct Row8 {
   row_u32x4 w[F32 ? 2 : 1];
