@@ -694,7 +694,10 @@ class GradSet:
     mx_grad_set): fp32 and bf16 CUDA tensors of one device, mixed as they come,
     contiguous or (1-D and 2-D) row-strided. It holds the tensors and their
     addresses: make another when one is replaced. It cannot be made while a
-    graph is captured (its table is copied to the device)."""
+    graph is captured (its table is copied to the device), and a captured graph
+    that uses it needs it for as long as the graph is replayed. It may be dropped
+    while a call on any stream still runs; a raw handle's stream has to live as
+    long as the set."""
 
     def __init__(self, tensors):
         import torch
@@ -723,9 +726,19 @@ class GradSet:
         _check(lib.mx_grad_set_fill(len(self.tensors), self._grads,
                                     self._host.data_ptr() if need.value else None, need.value,
                                     ctypes.byref(self.desc)), "mx_grad_set_fill")
+        self._table, self._home = None, 0
         if need.value:
+            self._home = torch.cuda.current_stream(self.device).cuda_stream
             self._table = self._host.to(self.device)
             self.desc.table = self._table.data_ptr()
+
+    def _used_on(self, handle: int) -> None:
+        """A call on the current stream, `handle`, reads the table: where that is
+        not the stream it was allocated for, its memory must not go to the next
+        allocation there, should the set be dropped, before this call is done."""
+        if handle != self._home and self._table is not None:
+            import torch
+            self._table.record_stream(torch.cuda.current_stream(self.device))
 
 
 def _grads_and_device(grads):
@@ -762,6 +775,7 @@ def grad_norm(grads, stream=None):
     place, handle = _place(device, stream)
     with place:
         s = _as_set(grads)
+        s._used_on(handle)
         norm, work, size = _norm_buffers(device, lib)
         st = lib.mx_grad_norm(s.desc, norm.data_ptr(), work.data_ptr(), size, handle)
     _check(st, "mx_grad_norm")
@@ -783,6 +797,9 @@ def clip_grad_norm(grads, max_norm: float, out=None, stream=None):
     with place:
         s = _as_set(grads)
         o = s if out is None else _as_set(out)
+        s._used_on(handle)
+        if o is not s:
+            o._used_on(handle)
         norm, work, size = _norm_buffers(device, lib)
         st = lib.mx_grad_clip(s.desc, o.desc, max_norm,
                               norm.data_ptr(), work.data_ptr(), size, handle)
