@@ -493,9 +493,9 @@ mx_status mx_grad_set_size(int32_t count, const mx_grad *grads, size_t *table_by
  * may be empty. The table holds the tensors' addresses: a tensor that moves
  * needs a new set.
  *  host_table  >= table_bytes, 8-byte aligned.
- * Errors: MX_ERR_NULL, MX_ERR_ARG (dtype, count < 0, the same memory twice: a
- * tensor without gaps that overlaps another such, or a tensor with gaps that
- * is given twice), MX_ERR_SHAPE (negative extents, ld < cols), MX_ERR_ALIGN
+ * Errors: MX_ERR_NULL, MX_ERR_ARG (dtype, count < 0, the same memory twice: an
+ * element that two tensors share; slices of one buffer that lie in each other's
+ * gaps share none), MX_ERR_SHAPE (negative extents, ld < cols), MX_ERR_ALIGN
  * (data not aligned to its elements), MX_ERR_UNSUPPORTED (more than 2^31
  * chunks, or a tensor's span above 2^62 bytes).
  */

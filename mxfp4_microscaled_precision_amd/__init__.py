@@ -692,7 +692,7 @@ def rmsnorm_backward(dy, h, rstd, weight, dres=None, dh=None, stream=None):
 class GradSet:
     """Gradient tensors laid out once for grad_norm and clip_grad_norm (see
     mx_grad_set): fp32 and bf16 CUDA tensors of one device, mixed as they come,
-    contiguous or (1-D and 2-D) row-strided. It holds the tensors and their
+    contiguous or (1-D and 2-D) row-strided, no element in two of them. It holds the tensors and their
     addresses: make another when one is replaced. It cannot be made while a
     graph is captured (its table is copied to the device), and a captured graph
     that uses it needs it for as long as the graph is replayed. It may be dropped

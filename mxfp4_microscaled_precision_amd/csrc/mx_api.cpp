@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <utility>
 
 #include "../../include/mxfp4.h"
 #include "mx_kernels.h"
@@ -547,22 +548,86 @@ mx_status mx_rmsnorm_backward(const mx_norm_grad *g, void *workspace, size_t wor
 
 namespace {
 
-// A set's table: the tensors, the chunks, then the indices of the tensors
-// without gaps by address (host only, for the overlap checks).
+// A set's table: the tensors, the chunks, then the indices of the tensors that
+// are not empty, those without gaps by address and then those with gaps by
+// address (host only, for the overlap checks).
 struct GradLayout {
-  int64_t chunks, chunk, ordered;
+  int64_t chunks, chunk, gapless, gapped;
   size_t chunks_at, order_at, bytes;
 };
 
 static bool grad_empty(const mx_grad &g) { return g.rows == 0 || g.cols == 0; }
 static bool grad_gapless(const mx_grad &g) { return g.rows <= 1 || g.ld == g.cols; }
 static int64_t grad_bytes(const mx_grad &g) { return g.rows * g.cols * dtype_size(g.dtype); }
+static uintptr_t address(const mx_grad &g) { return reinterpret_cast<uintptr_t>(g.data); }
+
+// A tensor's memory: count runs of `width` bytes, `pitch` apart (one run where
+// there are no gaps).
+struct GradRuns {
+  uintptr_t start;
+  int64_t count, width, pitch;
+  uintptr_t end() const { return start + (uintptr_t)((count - 1) * pitch + width); }
+};
+
+static GradRuns grad_runs(const mx_grad &g) {
+  if (grad_gapless(g)) return {address(g), 1, grad_bytes(g), grad_bytes(g)};
+  const int64_t size = dtype_size(g.dtype);
+  return {address(g), g.rows, g.cols * size, g.ld * size};
+}
+
+// Whether two tensors that are not empty share a byte. Run i of one and run j of
+// the other with the same pitch lie d + (j - i) pitch apart, so the smallest
+// j - i that ends past the other's start decides; with unequal pitches that is
+// asked for each run of the tensor with fewer.
+static bool grads_overlap(const mx_grad &p, const mx_grad &q) {
+  GradRuns a = grad_runs(p), b = grad_runs(q);
+  if (a.end() <= b.start || b.end() <= a.start) return false;
+  if (a.count > b.count) std::swap(a, b);
+  auto meet = [&b](uintptr_t start, int64_t count, int64_t width) {   // runs of b's pitch
+    const int64_t d = (int64_t)(b.start - start);
+    const int64_t past = -b.width - d;                  // of k pitches: strictly more than this
+    int64_t k = past / b.pitch + (past % b.pitch < 0 ? 0 : 1);
+    k = std::max(k, -(count - 1));
+    return k <= b.count - 1 && d + k * b.pitch < width;
+  };
+  if (a.count == 1 || a.pitch == b.pitch) return meet(a.start, a.count, a.width);
+  for (int64_t i = 0; i < a.count; ++i)
+    if (meet(a.start + (uintptr_t)(i * a.pitch), 1, a.width)) return true;
+  return false;
+}
+
+// Tensors by address.
+struct GradOrder {
+  const mx_grad *grads;
+  const uint32_t *index;
+  int64_t n;
+};
+
+// Whether a tensor of y starts within the span of one of x and shares memory
+// with it, unless it is the same one at the same place of its set.
+static bool any_clash(const GradOrder &x, const GradOrder &y) {
+  const uint32_t *const end = y.index + y.n;
+  for (int64_t i = 0; i < x.n && y.n > 0; ++i) {
+    const mx_grad &p = x.grads[x.index[i]];
+    const uintptr_t past = grad_runs(p).end();
+    const uint32_t *j =
+        std::lower_bound(y.index, end, address(p),
+                         [&](uint32_t e, uintptr_t at) { return address(y.grads[e]) < at; });
+    for (; j != end && address(y.grads[*j]) < past; ++j) {
+      const mx_grad &q = y.grads[*j];
+      const bool same = x.index[i] == *j && p.data == q.data &&
+                        grad_runs(p).pitch == grad_runs(q).pitch;
+      if (!same && grads_overlap(p, q)) return true;
+    }
+  }
+  return false;
+}
 
 static mx_status grad_layout(int32_t count, const mx_grad *grads, GradLayout *l) {
   if (count < 0) return MX_ERR_ARG;
   if (count > 0 && grads == nullptr) return MX_ERR_NULL;
   int64_t total = 0;
-  l->ordered = 0;
+  l->gapless = l->gapped = 0;
   for (int32_t i = 0; i < count; ++i) {
     const mx_grad &g = grads[i];
     if (!valid_dtype(g.dtype)) return MX_ERR_ARG;
@@ -576,7 +641,7 @@ static mx_status grad_layout(int32_t count, const mx_grad *grads, GradLayout *l)
     if (pitch > (((int64_t)1 << 62) / dtype_size(g.dtype)) / g.rows) return MX_ERR_UNSUPPORTED;
     total += g.rows * g.cols;
     if (total > ((int64_t)1 << 60)) return MX_ERR_UNSUPPORTED;
-    if (grad_gapless(g)) ++l->ordered;
+    ++(grad_gapless(g) ? l->gapless : l->gapped);
   }
   // Elements per chunk: enough chunks for every workgroup to walk several, and
   // none so small that looking it up shows: 0.7 M elements 8.5 us with 2048
@@ -590,7 +655,7 @@ static mx_status grad_layout(int32_t count, const mx_grad *grads, GradLayout *l)
   if (l->chunks > ((int64_t)1 << 31)) return MX_ERR_UNSUPPORTED;
   l->chunks_at = (size_t)count * sizeof(mx::GradTensor);
   l->order_at = l->chunks_at + (size_t)l->chunks * sizeof(mx::GradChunk);
-  l->bytes = l->order_at + (size_t)((l->ordered + 1) / 2 * 2) * sizeof(uint32_t);
+  l->bytes = l->order_at + (size_t)((l->gapless + l->gapped + 1) / 2 * 2) * sizeof(uint32_t);
   return MX_OK;
 }
 
@@ -635,8 +700,6 @@ static const uint32_t *grad_order(const mx_grad_set *s, int64_t *n) {
   return reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(s->host_table) + at);
 }
 
-static uintptr_t address(const mx_grad &g) { return reinterpret_cast<uintptr_t>(g.data); }
-
 // Whether tensors of two sets share memory other than place by place: both
 // sets' tensors without gaps, merged by address.
 static bool grad_sets_clash(const mx_grad_set *a, const mx_grad_set *b) {
@@ -680,28 +743,21 @@ mx_status mx_grad_set_fill(int32_t count, const mx_grad *grads, void *host_table
   if (table_bytes < l.bytes) return MX_ERR_SHAPE;
   if (!aligned(host_table, 8)) return MX_ERR_ALIGN;
   uint8_t *base = static_cast<uint8_t *>(host_table);
-  // Tensors with gaps only clash here when the same one is given twice (column
-  // slices of one buffer do not): sort them in the order's place, look, then
-  // sort the others.
   uint32_t *order = reinterpret_cast<uint32_t *>(base + l.order_at);
-  auto by_address = [&](uint32_t i, uint32_t j) { return address(grads[i]) < address(grads[j]); };
-  int64_t n = 0;
+  uint32_t *plain = order, *gaps = order + l.gapless;
   for (int32_t i = 0; i < count; ++i)
-    if (!grad_empty(grads[i]) && grad_gapless(grads[i])) order[n++] = (uint32_t)i;
-  std::sort(order, order + n, by_address);
-  for (int64_t i = 1; i < n; ++i)
+    if (!grad_empty(grads[i])) *(grad_gapless(grads[i]) ? plain : gaps)++ = (uint32_t)i;
+  auto by_address = [&](uint32_t i, uint32_t j) { return address(grads[i]) < address(grads[j]); };
+  std::sort(order, order + l.gapless, by_address);
+  std::sort(order + l.gapless, order + l.gapless + l.gapped, by_address);
+  for (int64_t i = 1; i < l.gapless; ++i)
     if (address(grads[order[i - 1]]) + (uintptr_t)grad_bytes(grads[order[i - 1]]) >
         address(grads[order[i]]))
       return MX_ERR_ARG;
+  const GradOrder without{grads, order, l.gapless}, with{grads, order + l.gapless, l.gapped};
+  if (any_clash(with, with) || any_clash(with, without) || any_clash(without, with))
+    return MX_ERR_ARG;
   mx::GradTensor *t = reinterpret_cast<mx::GradTensor *>(base);
-  // the tensors' place holds the ones with gaps while they are compared
-  uint32_t *gaps = reinterpret_cast<uint32_t *>(t);
-  int64_t m = 0;
-  for (int32_t i = 0; i < count; ++i)
-    if (!grad_empty(grads[i]) && !grad_gapless(grads[i])) gaps[m++] = (uint32_t)i;
-  std::sort(gaps, gaps + m, by_address);
-  for (int64_t i = 1; i < m; ++i)
-    if (address(grads[gaps[i - 1]]) == address(grads[gaps[i]])) return MX_ERR_ARG;
   mx::GradChunk *c = reinterpret_cast<mx::GradChunk *>(base + l.chunks_at);
   for (int32_t i = 0; i < count; ++i) {
     const mx_grad &g = grads[i];
