@@ -526,8 +526,7 @@ mx_status mx_grad_norm(const mx_grad_set *set, float *norm, void *workspace,
  * `out` is a set of the same shapes and types as `in`, or `in` itself (the same
  * set, or NULL) to clip in place; in place nothing is written while the norm is
  * within max_norm. A tensor of `out` is the tensor of `in` at the same place of
- * its set, or shares no memory with any of them (refused where both have no
- * gaps, the caller's to see to where one has).
+ * its set (same address and gaps), or shares no element with any of them.
  * A NaN norm makes every element NaN; an infinite one turns finite elements
  * into zeros and infinite ones into NaN (norm tells).
  *  max_norm   >= 0 (infinity: scale nothing).

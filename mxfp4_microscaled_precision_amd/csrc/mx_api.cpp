@@ -616,6 +616,7 @@ static bool any_clash(const GradOrder &x, const GradOrder &y) {
     for (; j != end && address(y.grads[*j]) < past; ++j) {
       const mx_grad &q = y.grads[*j];
       const bool same = x.index[i] == *j && p.data == q.data &&
+                        grad_runs(p).count == grad_runs(q).count &&
                         grad_runs(p).pitch == grad_runs(q).pitch;
       if (!same && grads_overlap(p, q)) return true;
     }
@@ -690,23 +691,26 @@ static mx::GradTable grad_table(const mx_grad_set *s) {
   return t;
 }
 
-// The tensors without gaps of a filled set, by address.
-static const uint32_t *grad_order(const mx_grad_set *s, int64_t *n) {
-  const size_t at = (size_t)s->count * sizeof(mx::GradTensor) +
-                    (size_t)s->chunks * sizeof(mx::GradChunk);
-  *n = 0;
+// The tensors of a filled set by address, those without gaps and those with.
+static void grad_orders(const mx_grad_set *s, GradOrder *without, GradOrder *with) {
+  const uint32_t *order = reinterpret_cast<const uint32_t *>(
+      static_cast<const uint8_t *>(s->host_table) + (size_t)s->count * sizeof(mx::GradTensor) +
+      (size_t)s->chunks * sizeof(mx::GradChunk));
+  int64_t n[2] = {0, 0};
   for (int32_t i = 0; i < s->count; ++i)
-    *n += !grad_empty(s->grads[i]) && grad_gapless(s->grads[i]);
-  return reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(s->host_table) + at);
+    if (!grad_empty(s->grads[i])) ++n[grad_gapless(s->grads[i])];
+  *without = {s->grads, order, n[1]};
+  *with = {s->grads, order + n[1], n[0]};
 }
 
-// Whether tensors of two sets share memory other than place by place: both
-// sets' tensors without gaps, merged by address.
+// Whether tensors of two sets of the same shapes share memory other than place
+// by place. Those without gaps are merged by address.
 static bool grad_sets_clash(const mx_grad_set *a, const mx_grad_set *b) {
-  int64_t na, nb;
-  const uint32_t *oa = grad_order(a, &na), *ob = grad_order(b, &nb);
-  for (int64_t i = 0, j = 0; i < na && j < nb;) {
-    const mx_grad &p = a->grads[oa[i]], &q = b->grads[ob[j]];
+  GradOrder x, xg, y, yg;
+  grad_orders(a, &x, &xg);
+  grad_orders(b, &y, &yg);
+  for (int64_t i = 0, j = 0; i < x.n && j < y.n;) {
+    const mx_grad &p = a->grads[x.index[i]], &q = b->grads[y.index[j]];
     const uintptr_t pe = address(p) + (uintptr_t)grad_bytes(p);
     const uintptr_t qe = address(q) + (uintptr_t)grad_bytes(q);
     if (pe <= address(q)) {
@@ -714,12 +718,13 @@ static bool grad_sets_clash(const mx_grad_set *a, const mx_grad_set *b) {
     } else if (qe <= address(p)) {
       ++j;
     } else {
-      if (oa[i] != ob[j] || p.data != q.data) return true;
+      if (x.index[i] != y.index[j] || p.data != q.data) return true;
       ++i;
       ++j;
     }
   }
-  return false;
+  return any_clash(xg, y) || any_clash(xg, yg) || any_clash(x, yg) || any_clash(yg, x) ||
+         any_clash(yg, xg) || any_clash(y, xg);
 }
 
 }  // namespace
@@ -799,8 +804,6 @@ mx_status mx_grad_clip(const mx_grad_set *in, const mx_grad_set *out, float max_
   st = check_set(out);
   if (st != MX_OK) return st;
   if (!(max_norm >= 0.0f)) return MX_ERR_ARG;
-  st = check_norm_outputs(norm, workspace, workspace_bytes);
-  if (st != MX_OK) return st;
   if (out != in) {
     if (out->count != in->count || out->chunks != in->chunks || out->chunk != in->chunk)
       return MX_ERR_MISMATCH;
@@ -810,6 +813,8 @@ mx_status mx_grad_clip(const mx_grad_set *in, const mx_grad_set *out, float max_
     }
     if (grad_sets_clash(in, out)) return MX_ERR_ARG;
   }
+  st = check_norm_outputs(norm, workspace, workspace_bytes);
+  if (st != MX_OK) return st;
   return hip_status(mx::grad_clip_launch(grad_table(in), grad_table(out),
                                          static_cast<double *>(workspace), max_norm, norm,
                                          static_cast<hipStream_t>(stream)));

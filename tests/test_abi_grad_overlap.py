@@ -86,3 +86,60 @@ def test_within_a_set_against_enumeration(lib):
         assert _fill(lib, entries)[0] == want, entries
         seen[want] += 1
     assert min(seen.values()) > 400, seen
+
+
+def _clip(lib, a, b):
+    """Status of clipping set a into set b with a misaligned norm, which is
+    refused (-3) after the sets and before anything is launched."""
+    sets = []
+    for entries in (a, b):
+        st, s, borrowed = _fill(lib, entries)
+        assert st == 0
+        s.table = P
+        sets.append((s, borrowed))
+    (x, _), (y, _) = sets
+    return lib.mx_grad_clip(ctypes.byref(x), ctypes.byref(y), 1.0, P + 2, P,
+                            lib.mx_grad_workspace(), None)
+
+
+FAR = P + (1 << 24)
+PAIRS = [
+    (-3, [(P, 8, 5, 20, 0)], [(P, 8, 5, 20, 0)]),               # in place
+    (-3, [(P, 8, 5, 20, 0)], [(P + 20, 8, 5, 20, 0)]),          # buf[:, :5] into buf[:, 5:10]
+    (-4, [(P, 8, 5, 20, 0)], [(P + 16, 8, 5, 20, 0)]),          # into buf[:, 4:9]
+    (-4, [(P, 8, 5, 20, 0)], [(P, 8, 5, 21, 0)]),               # same address, another pitch
+    (-4, [(P, 8, 5, 20, 0)], [(P, 8, 5, 5, 0)]),                # ... or without gaps
+    (-4, [(P, 8, 5, 5, 0)], [(P, 8, 5, 20, 0)]),
+    (-4, [(P, 8, 5, 20, 0)], [(P + 40, 8, 5, 5, 0)]),
+    (-3, [(P, 2, 5, 20, 0)], [(P + 20, 2, 5, 5, 0)]),           # within the first gap
+    (-3, [(P + 20, 2, 5, 5, 0)], [(P, 2, 5, 20, 0)]),
+    (-4, [(P, 2, 5, 20, 0), (FAR, 2, 5, 20, 0)], [(FAR, 2, 5, 20, 0), (P, 2, 5, 20, 0)]),
+    (-3, [(P, 2, 5, 20, 0), (FAR, 2, 5, 20, 0)], [(P, 2, 5, 20, 0), (FAR, 2, 5, 20, 0)]),
+    (-3, [(P, 2, 5, 20, 0), (P + 20, 2, 5, 20, 0), (FAR, 4, 4, 4, 0)],
+     [(P, 2, 5, 20, 0), (P + 20, 2, 5, 20, 0), (FAR, 4, 4, 4, 0)]),
+    (-4, [(P, 2, 5, 20, 0), (P + 20, 2, 5, 20, 0)], [(P, 2, 5, 20, 0), (P + 20, 2, 5, 40, 0)]),
+]
+
+
+@pytest.mark.parametrize("want,a,b", PAIRS)
+def test_between_sets(lib, want, a, b):
+    assert _clip(lib, a, b) == want
+
+
+def test_between_sets_against_enumeration(lib):
+    """A random tensor of one set over its place of the other, over another's or
+    beside all, against their bytes one by one."""
+    rng = random.Random(4)
+    seen = {-3: 0, -4: 0}
+    for _ in range(4000):
+        a = _random_entries(rng, 2)
+        b = [(e[0] if rng.random() < 0.5 else P + rng.randrange(60) * 4, e[1], e[2],
+              e[3] if rng.random() < 0.7 else e[2] + rng.randrange(6), e[4]) for e in a]
+        if _fill(lib, a)[0] != 0 or _fill(lib, b)[0] != 0:
+            continue
+        runs = lambda e: (e[0], e[3] if e[1] > 1 else 0)  # noqa: E731
+        want = -4 if any(_bytes(a[i]) & _bytes(b[j]) and not (i == j and runs(a[i]) == runs(b[j]))
+                         for i in range(2) for j in range(2)) else -3
+        assert _clip(lib, a, b) == want, (a, b)
+        seen[want] += 1
+    assert min(seen.values()) > 300, seen
