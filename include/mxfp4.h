@@ -528,8 +528,8 @@ mx_status mx_grad_norm(const mx_grad_set *set, float *norm, void *workspace,
  * within max_norm. A tensor of `out` is the tensor of `in` at the same place of
  * its set (same address and gaps), or shares no element with any of them.
  * A NaN norm makes every element NaN; an infinite one turns finite elements
- * into zeros and infinite ones into NaN (norm tells).
- *  max_norm   >= 0 (infinity: scale nothing).
+ * into zeros and infinite ones into NaN under a finite max_norm (norm tells).
+ *  max_norm   >= 0 (infinity: no limit, coef is 1 for an infinite norm too).
  * Errors: as for mx_grad_norm, and MX_ERR_ARG (max_norm negative or NaN, or
  * memory shared between the sets as above), MX_ERR_MISMATCH (`out` of other
  * shapes or types).

@@ -244,9 +244,10 @@ __global__ __launch_bounds__(kThreads, kWavesPerSimd) void grad_scale_kernel(
   const double n = __builtin_sqrt(total_of(partial, groups, part));
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
   // a norm that is NaN makes every element NaN; an infinite one zeroes the
-  // finite elements
+  // finite elements, but not where max_norm is infinite too (no limit)
   const double q = (double)max_norm / (n + 1e-6);
-  const float coef = q > 1.0 ? 1.0f : (float)q;
+  const bool within = q > 1.0 || (max_norm == __builtin_inff() && n == __builtin_inf());
+  const float coef = within ? 1.0f : (float)q;
   if (coef == 1.0f && in.tensors == out.tensors) return;   // nothing changes in place
   const int64_t last = in.chunks - 1;
   Chunk next = chunk_at(in, last - blockIdx.x);           // from the end, see grad_clip_launch

@@ -63,4 +63,6 @@ def clip_ref(grads: Sequence[np.ndarray], max_norm: float):
     norm = grad_norm_ref(grads)
     with np.errstate(all="ignore"):
         coef = np.minimum(1.0, np.float64(max_norm) / (norm + CLIP_EPS))   # NaN stays NaN
+        if np.isinf(max_norm) and not np.isnan(norm):
+            coef = 1.0                                                     # no limit
         return norm, [np.asarray(g, np.float64) * coef for g in grads]

@@ -271,3 +271,23 @@ def test_binding_refusals(mx):
     # the same tensors in another set: in place, tensor by tensor
     mx.clip_grad_norm(mx.GradSet([a]), 1.0, out=mx.GradSet([a]))
     assert abs(float(mx.grad_norm([a])) - 1.0) < 1e-5
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_no_limit(mx, bf16):
+    """An infinite max_norm scales nothing, also where the norm is infinite; a
+    NaN norm still shows in every element."""
+    import torch
+    v = np.ones((3, 40), np.float32)
+    v[1, 7], v[2, 3] = np.inf, -np.inf
+    norm, ref = oracle.clip_ref([v], float("inf"))
+    assert np.isinf(norm) and np.array_equal(ref[0], v)
+    g, out = [dev(v, bf16)], [dev(0 * np.ones_like(v), bf16)]
+    assert torch.isinf(mx.clip_grad_norm(g, float("inf"), out=out))
+    assert np.array_equal(host(out[0]), v)
+    assert torch.isinf(mx.clip_grad_norm(g, float("inf")))
+    assert np.array_equal(host(g[0]), v)
+    v[0, 0] = np.nan
+    g = [dev(v, bf16)]
+    assert torch.isnan(mx.clip_grad_norm(g, float("inf"))) and torch.isnan(g[0]).all()
+    assert np.isnan(oracle.clip_ref([v], float("inf"))[1][0]).all()
