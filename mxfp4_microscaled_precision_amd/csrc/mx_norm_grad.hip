@@ -247,15 +247,17 @@ __global__ __launch_bounds__(1024) void norm_grad_few_kernel(NormGradArgs a) {
   }
 }
 
-// dweight[c] = sum of the partial rows, in 64 bits: 32 columns per workgroup,
-// 32 threads to a column, all of a thread's loads in flight together.
+// dweight[c] = sum of the partial rows (cols apart), c < width, in 64 bits: 32
+// columns per workgroup, 32 threads to a column, all of a thread's loads in
+// flight together.
 __global__ __launch_bounds__(1024) void norm_grad_sum_kernel(const float *partial, int groups,
-                                                             int64_t cols, float *dweight) {
+                                                             int64_t cols, int64_t width,
+                                                             float *dweight) {
   __shared__ double part[32][33];
   const int c = threadIdx.x & 31, t = threadIdx.x >> 5;
   const int64_t col = (int64_t)blockIdx.x * 32 + c;
   double s = 0.0;
-  if (col < cols) {
+  if (col < width) {
     const float *p = partial + col;
     int g = t;
     for (; g + 7 * 32 < groups; g += 8 * 32) {
@@ -273,7 +275,7 @@ __global__ __launch_bounds__(1024) void norm_grad_sum_kernel(const float *partia
   double v = part[c][t];
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) v += __shfl_xor(v, m);
-  if (c == 0 && (int64_t)blockIdx.x * 32 + t < cols) dweight[(int64_t)blockIdx.x * 32 + t] = (float)v;
+  if (c == 0 && (int64_t)blockIdx.x * 32 + t < width) dweight[(int64_t)blockIdx.x * 32 + t] = (float)v;
 }
 
 // One unit of eight columns per thread up to 8192 columns, two of bf16 rows up
@@ -303,9 +305,14 @@ hipError_t launch_grad(const NormGradArgs &a, hipStream_t stream) {
     else
       e = launch(norm_grad_wide_kernel<F32>, grid, dim3(threads), 0, stream, a);
   }
-  if (e != hipSuccess) return e;
-  return launch(norm_grad_sum_kernel, dim3((unsigned)((a.cols + 31) / 32)), dim3(1024), 0, stream,
-                a.partial, (int)grid.x, a.cols, a.dweight);
+  // a launch holds fewer than 2^32 threads: 2^26 columns take half of that
+  constexpr int64_t kSumCols = (int64_t)1 << 26;
+  for (int64_t c = 0; c < a.cols && e == hipSuccess; c += kSumCols) {
+    const int64_t width = std::min(kSumCols, a.cols - c);
+    e = launch(norm_grad_sum_kernel, dim3((unsigned)((width + 31) / 32)), dim3(1024), 0, stream,
+               a.partial + c, (int)grid.x, a.cols, width, a.dweight + c);
+  }
+  return e;
 }
 
 }  // namespace

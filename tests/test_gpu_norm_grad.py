@@ -220,3 +220,34 @@ def test_binding_refusals(mx):
     with pytest.raises(mx.MxError) as e:
         mx.rmsnorm_backward(x[:, :60].contiguous(), x[:, :60].contiguous(), r, w[:60])
     assert e.value.status == -2
+
+
+@pytest.mark.parametrize("rows", [0, 2])
+def test_more_columns_than_a_launch_s_threads(mx, rows):
+    """2^27 columns and more, 32 threads to a column in the weight gradient's
+    sum: a launch may hold fewer than 2^32 threads. Sampled columns against
+    fp64, with the bounds above."""
+    import torch
+    cols = (1 << 27) + 4104
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    dy, h, w = (torch.randn(s, generator=gen, device="cuda").bfloat16()
+                for s in ((rows, cols), (rows, cols), (cols,)))
+    rstd = torch.linspace(0.5, 2.0, rows, device="cuda")
+    dh, dw = mx.rmsnorm_backward(dy, h, rstd, w)
+    assert dh.shape == (rows, cols) and dw.shape == (cols,)
+    if rows == 0:
+        assert not dw.any()
+        return
+    xh = h.double() * rstd.double()[:, None]
+    g = dy.double() * w.double()
+    m, S = (v.mean(1, keepdim=True) for v in (g * xh, (g * xh).abs()))
+    pick = torch.cat([torch.arange(a, b, device="cuda") for a, b in
+                      ((0, 40), ((1 << 26) - 40, (1 << 26) + 40), ((1 << 27) - 40, (1 << 27) + 40),
+                       (cols - 40, cols))])
+    xh, g, rs, K = xh[:, pick], g[:, pick], rstd.double()[:, None], cols / 512 + 64
+    ref = rs * (g - xh * m)
+    bound = rs * (6 * U * (g.abs() + (xh * m).abs()) + xh.abs() * (K + 4) * U * S) \
+        + (2 * U + 2.0 ** -8) * ref.abs() + 2.0 ** -134
+    assert torch.all((dh[:, pick].double() - ref).abs() <= bound)
+    terms = dy[:, pick].double() * xh
+    assert torch.all((dw[pick].double() - terms.sum(0)).abs() <= 69 * U * terms.abs().sum(0))
