@@ -302,3 +302,38 @@ def test_binding_refusals(mx):
         with pytest.raises(mx.MxError) as e:
             bad()
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("rows,cols", [(8192, 4096), (4096, 8224)])
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("fmt,rnd,rotate", [("fp4_e2m1", "rne", "hadamard"),
+                                            ("fp4_e2m1", "sr", "rand_sign_hadamard"),
+                                            ("fp8_e4m3", "rne", "hadamard16")])
+def test_rows_read_past_the_caches(mx, fmt, rnd, rotate, bf16, rows, cols):
+    """Rows of 192 MB and more take kernels that read and write around the
+    caches: the first 512 rows come out as those rows alone do (checked against
+    the oracle at such sizes above). Tiles of 16 rows follow each other in the
+    axis-1 operand; in the axis-0 one the first 512 rows are the first K."""
+    import torch
+    some = 512
+    assert rows * cols * (2 if bf16 else 4) * 3 >= 192 << 20 > some * cols * 4 * 3
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    x, r = (torch.randn(rows, cols, generator=gen, device="cuda") for _ in range(2))
+    x, r = (x.bfloat16(), r.bfloat16()) if bf16 else (x, r)
+    w = 1 + 0.1 * torch.randn(cols, generator=gen, device="cuda")
+    for dual in (False, True):
+        kw = dict(format=fmt, rotate=rotate, round=rnd, seed1=5, seed0=6 | 1 << 32, dual=dual)
+        got = mx.rmsnorm_quantize(x, w, r, **kw)
+        want = mx.rmsnorm_quantize(x[:some], w, r[:some], **kw)
+        assert torch.equal(got.h, x + r) and torch.equal(got.rstd[:some], want.rstd)
+        n = want.q1.codes.numel()
+        assert torch.equal(got.q1.codes[:n], want.q1.codes)
+        shape = -1, 1024                        # scales: [K / 128][MN / 256][1024]
+        a, b = (q.q1.scales.view(-(-cols // 128), *shape) for q in (got, want))
+        assert torch.equal(a[:, :some // 256], b)
+        if dual:
+            tile = 2048 if fmt == "fp8_e4m3" else 1024    # [MN / 16][K / 128][tile]
+            a, b = (q.q0.codes.view(-1, k // 128, tile) for q, k in ((got, rows), (want, some)))
+            assert torch.equal(a[:, :some // 128], b)
+            a, b = (q.q0.scales.view(k // 128, -1) for q, k in ((got, rows), (want, some)))
+            assert torch.equal(a[:some // 128], b)

@@ -251,3 +251,29 @@ def test_more_columns_than_a_launch_s_threads(mx, rows):
     assert torch.all((dh[:, pick].double() - ref).abs() <= bound)
     terms = dy[:, pick].double() * xh
     assert torch.all((dw[pick].double() - terms.sum(0)).abs() <= 69 * U * terms.abs().sum(0))
+
+
+@pytest.mark.parametrize("dres", [True, False])
+@pytest.mark.parametrize("rows,cols", [(16384, 4096), (2800, 12288)])
+def test_rows_read_past_the_caches(mx, rows, cols, dres):
+    """bf16 rows of 192 MB and more, one unit of columns to a thread and two:
+    every element against fp64, with the bounds above."""
+    import torch
+    assert rows * cols * 2 * (4 if dres else 3) >= 192 << 20
+    gen = torch.Generator(device="cuda").manual_seed(rows + dres)
+    dy, h, w, d = (torch.randn(s, generator=gen, device="cuda").bfloat16()
+                   for s in ((rows, cols), (rows, cols), (cols,), (rows, cols)))
+    rstd = (h.double().square().mean(1) + 1e-5).rsqrt().float()
+    dh, dw = mx.rmsnorm_backward(dy, h, rstd, w, d if dres else None)
+    rs = rstd.double()[:, None]
+    xh, g = h.double() * rs, dy.double() * w.double()
+    m, S = ((g * xh).mean(1, keepdim=True), (g * xh).abs().mean(1, keepdim=True))
+    K = cols / 512 + 64
+    ref = rs * (g - xh * m) + (d.double() if dres else 0)
+    bound = rs * (6 * U * (g.abs() + (xh * m).abs()) + xh.abs() * (K + 4) * U * S) \
+        + (2 * U + 2.0 ** -8) * ref.abs() + 2.0 ** -134
+    if dres:
+        bound += 2 * U * d.double().abs()
+    assert torch.all((dh.double() - ref).abs() <= bound)
+    terms = dy.double() * xh
+    assert torch.all((dw.double() - terms.sum(0)).abs() <= (rows / 64 + 68) * U * terms.abs().sum(0))
