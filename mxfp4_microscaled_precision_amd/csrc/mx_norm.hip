@@ -127,10 +127,13 @@ __global__ __launch_bounds__(MAXW * 64, 4) void norm_axis1_kernel(NormArgs a) {
   auto part_col = [&](uint32_t u, int n) {
     return (int64_t)u * kUnitCols + n * (kUnitCols / kParts) + lane * kPartCols;
   };
-  // Columns past the last: the lane reads the row's last ones (bf16) or nothing
-  // (fp32, where a lane may be past with its second part alone). Each is the
-  // faster one for its type: 512 x 4096 bf16 6.5 us against 6.9 us by a branch,
-  // 8192 x 4096 fp32 78.6 us by the branch against 89.7 us.
+  // Columns past the last, which only padding sees: fp32 takes zeros by a branch
+  // in each load (a lane may be past with its second part alone), bf16 takes
+  // zeros by one branch around a unit's first reading (read_unit) and the row's
+  // last columns in its second. Each is the faster one for its type: 512 x 4096
+  // bf16 6.6 us against 6.9 us by the branch in each load, 8192 x 4096 fp32
+  // 78.6 us by it against 89.7 us. (The zeros of read_unit, which keep h from
+  // being used without a value, are 0.05 us of the 6.6.)
   auto load_row = [&](const void *p, int64_t row0, uint32_t u, auto once) {
     Row8<F32> v;
 #pragma unroll
@@ -144,7 +147,11 @@ __global__ __launch_bounds__(MAXW * 64, 4) void norm_axis1_kernel(NormArgs a) {
   // held (a std::bool_constant): h is not read again here and is written past
   // the caches
   auto read_unit = [&](uint32_t u, Row8<F32>(&v)[4], auto held) {
-    if (!F32 && part_col(u, 0) >= a.cols) return;
+    if (!F32 && part_col(u, 0) >= a.cols) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j].w[0] = row_u32x4{0u, 0u, 0u, 0u};
+      return;
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       v[j] = load_row(a.x, min(r0 + j, a.rows - 1) * a.ldx, u, std::bool_constant<ONCE>{});
