@@ -518,8 +518,9 @@ def _place(device, stream):
     still be using."""
     import torch
     if stream is None:
-        # torch.cuda.current_stream(device).cuda_stream without its stream object
-        handle = torch._C._cuda_getCurrentRawStream(device.index)
+        # current_stream without its stream object, where torch still has that
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        handle = raw(device.index) if raw else torch.cuda.current_stream(device).cuda_stream
         here = device.index == torch.cuda.current_device()
         return (_HERE if here else torch.cuda.device(device)), handle
     if not hasattr(stream, "cuda_stream"):

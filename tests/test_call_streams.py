@@ -1,5 +1,6 @@
-"""A gradient set's device table while calls on other streams than its own
-read it: the set may be dropped as soon as the call returns."""
+"""Calls and their streams: a gradient set's device table while calls on other
+streams than its own read it (the set may be dropped as soon as the call
+returns), and the handle of the current stream."""
 import contextlib
 import types
 
@@ -72,3 +73,20 @@ def test_dropped_while_a_side_stream_runs(mx, raw):
     norm = 2.0 * 1000 ** 0.5
     # coef and the product round once each
     assert torch.all((out.double() - 2.0 / (norm + 1e-6)).abs() <= 2 * 2.0 ** -24 * 2.0 / norm)
+
+
+@pytest.mark.parametrize("shortcut", [True, False])
+def test_current_stream_with_and_without_torch_s_shortcut(monkeypatch, shortcut):
+    """The handle of the current stream comes from a private function of torch,
+    or from the public one where that is gone (stand-ins, no GPU)."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream",
+                        lambda device=None: types.SimpleNamespace(cuda_stream=9))
+    if shortcut:
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 8, raising=False)
+    else:
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    place, handle = mx_package._place(torch.device("cuda", 0), None)
+    assert handle == (8 if shortcut else 9)
+    with place:
+        pass
