@@ -357,6 +357,9 @@ mx_status mx_dequantize(const mx_qtensor *q, float *out, int64_t ld, void *strea
  *     y    = (h * rstd) * weight                (fp32)
  * y is then rotated, scaled and rounded as mx_quantize does with its source,
  * except that y enters in fp32: it is never rounded to bf16 and never written.
+ * With nearest rounding after a rotation, a value below 2^-126 in a block whose
+ * largest is below 2^-106 is multiplied by the rotation's factor and the scale
+ * in one rounding, not in two, and may so get the neighbouring code.
  *
  *  x          device [rows, cols], leading dimension ldx (elements), `dtype`.
  *  residual   device [rows, cols], ldr, or NULL for none. Without it h is x
@@ -524,8 +527,8 @@ mx_status mx_grad_norm(const mx_grad_set *set, float *norm, void *workspace,
  *     out = in * coef      (rounded to the tensor's type)
  *     norm[0] = the norm before clipping
  * `out` is a set of the same shapes and types as `in`, or `in` itself (the same
- * set, or NULL) to clip in place; in place nothing is written while the norm is
- * within max_norm. A tensor of `out` is the tensor of `in` at the same place of
+ * set, or NULL) to clip in place; in place nothing is written while coef rounds
+ * to 1 in fp32. A tensor of `out` is the tensor of `in` at the same place of
  * its set (same address and gaps), or shares no element with any of them.
  * A NaN norm makes every element NaN; an infinite one turns finite elements
  * into zeros and infinite ones into NaN under a finite max_norm (norm tells).

@@ -103,7 +103,10 @@ __device__ __forceinline__ void store_one(gbyte *p, float v) {
 // A chunk's elements as contiguous runs: the whole chunk of a tensor without
 // gaps, else the piece of each row. f(first element within the tensor's
 // buffer, within the tensor, elements, thread, threads); a run of a tensor
-// with gaps goes to one wave, a whole chunk to the workgroup.
+// with gaps goes to one wave, a whole chunk to the workgroup. Rows of fewer than
+// a wave's units leave lanes idle: norm and scaling of 67 MB in fp32 rows of 256
+// take 49 us, but of 33.5 MB in bf16 rows of 64 105 us, of 4 MB in single
+// elements 487 us.
 template <typename F>
 __device__ __forceinline__ void for_runs(const GradTensor &t, int64_t ld, int64_t first,
                                          int64_t len, F f) {

@@ -69,9 +69,11 @@ __device__ __forceinline__ void widen_weight(const Row8<1> &r, int f32, float (&
 // The block of y of row r at K = 32 kb of the axis-1 operand, rotated (random
 // signs: mask) and rounded; returns its scale code. The stochastic rounding
 // index is L = r * cols + 32 kb + i (cols % 32 == 0). quantize_block multiplies
-// once by c * 2^-e where the rule multiplies twice: for y of more bits than
-// bf16 the two agree unless a rotated value is subnormal in fp32 (below
-// 2^-126), where they may pick different neighbours of a tie.
+// once by c * 2^-e where the rule multiplies twice (nearest rounding): for y of
+// more bits than bf16 the two agree unless the value times c is subnormal in
+// fp32 (below 2^-126), where they may come out on different sides of a rounding
+// border. Such a value has a code other than 0 only in a block whose scale is
+// below 2^-115, its largest value below 2^-106 (E4M3; 2^-121 for E2M1).
 template <int ROT, int RND, int FMT, int kWords>
 __device__ __forceinline__ uint32_t encode_row_block(const NormArgs &a, float (&y)[32], int64_t r,
                                                      int64_t kb, uint32_t mask,

@@ -16,7 +16,11 @@
 //
 // 16384 x 4096 bf16 with dres: 85.4 us for 547 MB (6.4 TB/s: bound by HBM)
 // and 4.8 us for the second launch (8 MB of partial rows); before the next
-// row's loads overlapped the row sum the two took 106 and 32 us.
+// row's loads overlapped the row sum the two took 106 and 32 us. Wider rows are
+// further from their bytes at a copy's 5.4 TB/s: 2048 x 8192 29.8 us against
+// 24.9, 2048 x 12288 52.6 against 37.3 (one workgroup of sixteen waves to a
+// compute unit), fp32 117.7 against 74.6 and 1024 x 28672 96.3 against 43.5
+// (norm_grad_wide_kernel).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
