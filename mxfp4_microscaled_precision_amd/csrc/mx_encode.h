@@ -88,6 +88,20 @@ __device__ __forceinline__ float rot_norm() {
   return RK == 2 ? 0.25f : bits_f(kInvSqrt32Bits);
 }
 
+// max |v| of a block after the 32-point rotation, as bits: one v_maximum3_f32
+// for two elements, which keeps a NaN where v_max3_f32 skips it. A source block
+// that holds a NaN or Inf leaves no output finite, but one of finite values
+// whose sums overflow to both infinities can leave NaN beside finite outputs
+// and no Inf.
+__device__ __forceinline__ uint32_t rotated_amax(const float (&v)[32]) {
+  float m = fabsf(v[0]);
+#pragma unroll
+  for (int i = 1; i < 31; i += 2)
+    m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, fabsf(v[i])),
+                                      fabsf(v[i + 1]));
+  return f_bits(__builtin_elementwise_maximum(m, fabsf(v[31]))) & 0x7FFFFFFFu;
+}
+
 // Quantize one 32-element block. v holds the butterfly output h (RK != 0) or
 // the input x (RK == 0). The rotated value is y = fl32(h * c) with c the
 // normalisation (rot_norm).
@@ -118,21 +132,14 @@ __device__ __forceinline__ uint32_t quantize_block(const float (&v)[32],
                                                    uint32_t (&out)[FMT == kFmtE4M3 ? 8 : 4],
                                                    U24Fn u24_of) {
   constexpr int kWords = FMT == kFmtE4M3 ? 8 : 4;
-  // amax as bits of |v| (a NaN or Inf compares above 0x7f800000). Without
-  // the 32-point rotation: integer max of |bits|, which sees a lone NaN (the
-  // 16-point variant leaves one half finite when the other holds a NaN).
-  // With it every output of a block holding a NaN or Inf is itself NaN or
-  // Inf, so the float max of |v| (which skips NaN operands) still lands above
-  // 0x7f800000 for such blocks and equals the integer max for the others.
+  // amax as bits of |v| (a NaN or Inf compares above 0x7f800000): integer max
+  // of |bits|, or with the 32-point rotation the float max, see rotated_amax.
   uint32_t amax = 0;
   if (RK != 1) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) amax = max(amax, f_bits(v[i]) & 0x7FFFFFFFu);
   } else {
-    float m = fabsf(v[0]);
-#pragma unroll
-    for (int i = 1; i < 31; i += 2) m = fmaxf(fmaxf(m, fabsf(v[i])), fabsf(v[i + 1]));
-    amax = f_bits(fmaxf(m, fabsf(v[31])));
+    amax = rotated_amax(v);
   }
   const bool nonfinite = amax >= 0x7F800000u;
   const float c = rot_norm<RK>();
@@ -224,10 +231,7 @@ __device__ __forceinline__ uint32_t block_scale(const float (&v)[32], float &m1,
 #pragma unroll
     for (int i = 0; i < 32; ++i) amax = max(amax, f_bits(v[i]) & 0x7FFFFFFFu);
   } else {
-    float m = fabsf(v[0]);
-#pragma unroll
-    for (int i = 1; i < 31; i += 2) m = fmaxf(fmaxf(m, fabsf(v[i])), fabsf(v[i + 1]));
-    amax = f_bits(fmaxf(m, fabsf(v[31])));
+    amax = rotated_amax(v);
   }
   const bool nonfinite = amax >= 0x7F800000u;
   const float c = rot_norm<RK>();
