@@ -15,7 +15,10 @@
  * "Was ist MXFP4?"), rounded to nearest-even or stochastically.
  *
  * Around the linears stand the RMS norm of the residual stream into packed
- * operands, its gradient, and clipping by the global gradient norm.
+ * operands, its gradient, and clipping by the global gradient norm. The
+ * linears also come with an epilogue (bias, activation, gate, residual, and
+ * the gradient through the activation) and grouped by expert, over rows that
+ * are quantized in the router's order.
  *
  * Conventions for every call:
  *  - All tensor pointers are DEVICE pointers (hipMalloc / torch CUDA memory)
@@ -539,6 +542,181 @@ mx_status mx_grad_norm(const mx_grad_set *set, float *norm, void *workspace,
  */
 mx_status mx_grad_clip(const mx_grad_set *in, const mx_grad_set *out, float max_norm, float *norm,
                        void *workspace, size_t workspace_bytes, void *stream);
+
+/* Activation of an epilogue. */
+typedef enum mx_activation {
+  MX_ACT_NONE = 0,
+  MX_ACT_RELU = 1,
+  MX_ACT_SILU = 2,       /* z / (1 + e^-z)                                       */
+  MX_ACT_GELU = 3,       /* z Phi(z), Phi from a formula of absolute error 1.5e-7 */
+  MX_ACT_GELU_TANH = 4   /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2      */
+} mx_activation;
+
+/*
+ * What a product computes from its sums acc, in fp32 up to one rounding of each
+ * output to its type.
+ * Forward (gradient == 0):
+ *     z = acc + bias,   pre = z,   C = act(z) * mul + residual
+ * Gradient (gradient == 1): acc is the gradient of act(pre) * mul, and
+ *     C = acc * mul * act'(pre)   (the gradient of pre)
+ *     dmul = acc * act(pre)
+ * act' of relu is 0 at 0 and below. act of an infinity is its limit; NaN stays
+ * NaN.
+ *
+ *  bias      device [N] (one row of N per group in a grouped product), of
+ *            bias_dtype (mx_out_dtype); NULL: 0. Forward only.
+ *  mul       device, C's type and shape, leading dimension ldmul; NULL: 1.
+ *  residual  device, C's type and shape, ldres; NULL: 0. Forward only.
+ *  pre       device, C's type and shape, ldpre. Forward: written, or NULL.
+ *            Gradient: read, required.
+ *  dmul      device, C's type and shape, lddmul; written, or NULL. Gradient
+ *            with mul only.
+ * Matrices that are read may be C or another output itself (same pointer and
+ * leading dimension: an output is then written over what it was computed from)
+ * but overlap them in no other way. Alignment: their element size (16 bytes,
+ * with leading dimensions of 16 bytes, is faster).
+ */
+typedef struct mx_epilogue {
+  int32_t activation, gradient;
+  const void *bias;
+  int32_t bias_dtype;
+  const void *mul, *residual;
+  void *pre, *dmul;
+  int64_t ldmul, ldres, ldpre, lddmul;
+} mx_epilogue;
+
+/*
+ * mx_linear with an epilogue (NULL: none) on MXFP4 operands; arguments,
+ * requirements and limits otherwise as for mx_linear. With K == 0 the sums
+ * are 0. C may be the matrix that residual, mul or (gradient) pre points to,
+ * so a weight gradient is added onto an fp32 buffer with residual == C.
+ * Errors: as for mx_linear; MX_ERR_ARG also for an unknown activation, a bias or
+ * residual in a gradient, dmul without mul or outside a gradient, two outputs at
+ * one address; MX_ERR_NULL for a gradient without pre; MX_ERR_SHAPE for a
+ * leading dimension below N, or for matrices at one address with different
+ * leading dimensions; MX_ERR_UNSUPPORTED for MXFP8 operands.
+ */
+mx_status mx_linear_fused(int32_t op, const mx_qtensor *A, const mx_qtensor *B,
+                          const mx_epilogue *epilogue, void *C, int64_t ldc, int32_t out_dtype,
+                          void *stream);
+
+/*
+ * An operand whose source rows belong to `groups` groups that follow one
+ * another (the rows of each expert, or each expert's matrix).
+ *  q           the packed operand. q.axis == 1: an ordinary axis-1 operand
+ *              (mx_quantize, mx_rmsnorm_quantize, mx_quantize_grouped).
+ *              q.axis == MX_AXIS_GROUPED: the axis-0 operand of
+ *              mx_quantize_grouped: MN = cols, and along K each group's rows
+ *              begin a 128-deep slice of their own, with zeros behind its last
+ *              row; the layout is that of a K extent of 128 slices, where
+ *                slices = groups * ceil(group_rows / 128)       equal groups
+ *                       = floor((rows + 127 groups) / 128)      ragged ones
+ *              (what is behind the last group's slices is zero).
+ *  group_rows  >= 0: equal groups of that many rows (rows == groups *
+ *              group_rows). -1: ragged groups, whose ends the call is given.
+ */
+#define MX_AXIS_GROUPED 2
+typedef struct mx_grouped {
+  mx_qtensor q;
+  int32_t groups;
+  int64_t group_rows;
+} mx_grouped;
+
+/*
+ * Where mx_quantize_grouped finds its rows: row i of `rows` is row index[i] of
+ * x, or row i without an index. Groups: `groups` of `group_rows` rows each, or
+ * ragged ones (group_rows == -1) that end before the rows ends[0], ends[1], ..
+ * (device, written by whatever routed the rows; group 0 begins at row 0). An
+ * end below an earlier one counts as that one (an empty group), an end past the
+ * last row as the last row; rows behind the last end are in no group.
+ *  x           device bf16 [src_rows, cols], leading dimension ld, 16-byte
+ *              aligned, ld % 8 == 0, cols % 32 == 0.
+ *  index       device int32 (index_bits 32) or int64 (64) [rows], or NULL
+ *              (then src_rows == rows). The same row may come up any number of
+ *              times; an index outside [0, src_rows) gives a row of zeros.
+ *  ends        device int32 [groups]; NULL for equal groups.
+ */
+typedef struct mx_grouped_source {
+  const void *x;
+  int64_t src_rows, cols, ld;
+  const void *index;
+  int32_t index_bits;
+  int64_t rows;
+  int32_t groups;
+  int64_t group_rows;
+  const int32_t *ends;
+} mx_grouped_source;
+
+/*
+ * Byte sizes of the operands that mx_quantize_grouped writes: axis 1, or
+ * MX_AXIS_GROUPED. Host-only.
+ * Errors: MX_ERR_NULL, MX_ERR_ARG (axis, groups < 1), MX_ERR_SHAPE (negative
+ * extents, cols % 32, rows != groups * group_rows), MX_ERR_UNSUPPORTED (more
+ * than 65536 groups, extents above 2^31).
+ */
+mx_status mx_quantize_grouped_sizes(int64_t rows, int64_t cols, int32_t groups,
+                                    int64_t group_rows, int32_t axis, size_t *codes_bytes,
+                                    size_t *scales_bytes);
+
+/* Bytes of the workspace that mx_quantize_grouped needs for `sums`. Host-only;
+ * errors as above. */
+mx_status mx_quantize_grouped_workspace(int64_t rows, int64_t cols, int32_t groups,
+                                        int64_t group_rows, size_t *bytes);
+
+/*
+ * Rotate + quantize grouped rows into MXFP4: the operands of the grouped
+ * products, from one read of the rows. Each block is encoded as mx_quantize
+ * encodes it; blocks along the rows never hold rows of two groups.
+ *
+ *  block, rotate, round, seed1, seed0  as for mx_quantize_dual. In the grouped
+ *             axis-0 operand the random sign of a row is that of its place
+ *             within its group (so that every operand grouped alike has the
+ *             same ones); stochastic rounding draws by the place in `rows`.
+ *  codes1, scales1, desc1   the axis-1 operand of the rows, written in full;
+ *             rows in no group hold zeros.
+ *  codes0, scales0, desc0   the grouped axis-0 operand, or codes0 == scales0
+ *             == NULL for none (desc0 is then not written).
+ *  sums       device fp32 [groups, cols], 4-byte aligned: each group's column
+ *             sums (what the bias of a linear whose output gradient x is
+ *             gets), summed in fp32, 32 rows at a time; or NULL.
+ *  workspace  device, >= mx_quantize_grouped_workspace bytes, 16-byte aligned
+ *             (with sums only; as for mx_rmsnorm_backward).
+ * The descriptors may be NULL. rows == 0 writes zeros to sums; cols == 0
+ * launches nothing. Limits: each operand's padded codes below 1 GiB.
+ * Errors: MX_ERR_NULL, MX_ERR_ARG, MX_ERR_SHAPE (also a workspace that is too
+ * small), MX_ERR_ALIGN, MX_ERR_UNSUPPORTED, MX_ERR_HIP.
+ */
+mx_status mx_quantize_grouped(const mx_grouped_source *source, int32_t block, int32_t rotate,
+                              int32_t round, uint64_t seed1, uint64_t seed0, void *codes1,
+                              void *scales1, void *codes0, void *scales0, float *sums,
+                              void *workspace, size_t workspace_bytes, mx_grouped *desc1,
+                              mx_grouped *desc0, void *stream);
+
+/*
+ * The products of a linear per expert, in one launch:
+ *  op = MX_OP_FPROP: A = X [T, in] axis 1, ragged; B = W [groups * out, in]
+ *       axis 1, equal groups of out rows. Row t of C [T][out] is X's row times
+ *       its group's matrix, transposed.
+ *  op = MX_OP_DGRAD: A = dY [T, out] axis 1, ragged; B = W [groups * out, in]
+ *       MX_AXIS_GROUPED, equal groups of out rows. C [T][in].
+ *  op = MX_OP_WGRAD: A = dY [T, out], B = X [T, in], both MX_AXIS_GROUPED and
+ *       ragged with the same rows. C [groups * out][in]: each group's dY^T X,
+ *       zeros (and the epilogue's terms) for a group without rows.
+ *  ends     device int32 [groups], as in mx_grouped_source and, for a
+ *           MX_AXIS_GROUPED operand, with the values it was quantized with.
+ *           Rows of C (fprop, dgrad), and of pre and dmul, behind the last end
+ *           are left as they were.
+ *  epilogue may be NULL; its bias has one row per group.
+ * Operands and C otherwise as for mx_linear_fused. Every row's sum is over its
+ * own reduction extent only: a NaN block reaches the rows and matrices that
+ * reduce over it, no other group's.
+ * Errors: as for mx_linear_fused; MX_ERR_ARG also for operands with other axes
+ * or kinds of groups than op takes, MX_ERR_SHAPE for other numbers of groups or
+ * rows, MX_ERR_NULL for ends.
+ */
+mx_status mx_linear_grouped(int32_t op, const mx_grouped *A, const mx_grouped *B,
+                            const int32_t *ends, const mx_epilogue *epilogue, void *C,
+                            int64_t ldc, int32_t out_dtype, void *stream);
 
 /* Static, NUL-terminated name of a status code. Never NULL. */
 const char *mx_status_string(int32_t status);

@@ -17,7 +17,10 @@ durchbricht die bestehende Erkenntnis ...", section "Fehlerdiagnoseexperiment"):
 
 Around the linears of a training step: rmsnorm_quantize writes the packed
 operands of the normalised residual stream, rmsnorm_backward is its gradient,
-and clip_grad_norm scales the gradients by their global norm.
+and clip_grad_norm scales the gradients by their global norm. linear_fused
+computes a linear with its bias, activation, gate and residual in one launch,
+linear_act_backward the gradient through the activation, linear_grouped the
+linears of all experts over rows that quantize_grouped gathered.
 """
 from __future__ import annotations
 
@@ -34,7 +37,10 @@ __all__ = [
     "quantize_fp8_sizes", "quantize_fp8", "linear", "linear_batched", "dequantize",
     "NormDesc", "NormGradDesc", "GradDesc", "GradSetDesc", "RMSNormQuantized",
     "rmsnorm_quantize", "rmsnorm_backward", "GradSet", "grad_norm", "clip_grad_norm",
-    "ROTATE", "ROUND", "FORMATS", "OPS", "OUT_DTYPES", "OP_AXES",
+    "EpilogueDesc", "GroupedDesc", "GroupedSourceDesc", "GroupedQuantized", "packed_operand",
+    "quantize_grouped_sizes", "quantize_grouped", "linear_fused", "linear_act_backward",
+    "linear_grouped",
+    "ROTATE", "ROUND", "FORMATS", "OPS", "OUT_DTYPES", "OP_AXES", "ACTIVATIONS", "AXIS_GROUPED",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmxfp4.so")
@@ -46,6 +52,9 @@ OPS = {"fprop": 0, "dgrad": 1, "wgrad": 2}
 OUT_DTYPES = {"f32": 0, "bf16": 1}
 # (A axis, B axis) each op needs
 OP_AXES = {"fprop": (1, 1), "dgrad": (1, 0), "wgrad": (0, 0)}
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+# the axis of a grouped operand whose blocks run along its rows, group by group
+AXIS_GROUPED = 2
 
 MX_OK = 0
 
@@ -139,6 +148,49 @@ class GradSetDesc(ctypes.Structure):
     ]
 
 
+class EpilogueDesc(ctypes.Structure):
+    """Mirror of struct mx_epilogue in include/mxfp4.h."""
+    _fields_ = [
+        ("activation", ctypes.c_int32),
+        ("gradient", ctypes.c_int32),
+        ("bias", ctypes.c_void_p),
+        ("bias_dtype", ctypes.c_int32),
+        ("mul", ctypes.c_void_p),
+        ("residual", ctypes.c_void_p),
+        ("pre", ctypes.c_void_p),
+        ("dmul", ctypes.c_void_p),
+        ("ldmul", ctypes.c_int64),
+        ("ldres", ctypes.c_int64),
+        ("ldpre", ctypes.c_int64),
+        ("lddmul", ctypes.c_int64),
+    ]
+
+
+class GroupedDesc(ctypes.Structure):
+    """Mirror of struct mx_grouped in include/mxfp4.h."""
+    _fields_ = [
+        ("q", QTensorDesc),
+        ("groups", ctypes.c_int32),
+        ("group_rows", ctypes.c_int64),
+    ]
+
+
+class GroupedSourceDesc(ctypes.Structure):
+    """Mirror of struct mx_grouped_source in include/mxfp4.h."""
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("src_rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("ld", ctypes.c_int64),
+        ("index", ctypes.c_void_p),
+        ("index_bits", ctypes.c_int32),
+        ("rows", ctypes.c_int64),
+        ("groups", ctypes.c_int32),
+        ("group_rows", ctypes.c_int64),
+        ("ends", ctypes.c_void_p),
+    ]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 _SIGNATURES = {
@@ -201,6 +253,28 @@ _SIGNATURES = {
     "mx_grad_clip": (ctypes.c_int, [ctypes.POINTER(GradSetDesc), ctypes.POINTER(GradSetDesc),
                                     ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
                                     ctypes.c_size_t, ctypes.c_void_p]),
+    "mx_linear_fused": (ctypes.c_int, [ctypes.c_int32, ctypes.POINTER(QTensorDesc),
+                                       ctypes.POINTER(QTensorDesc),
+                                       ctypes.POINTER(EpilogueDesc), ctypes.c_void_p,
+                                       ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p]),
+    "mx_quantize_grouped_sizes": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32,
+                                                 ctypes.c_int64, ctypes.c_int32,
+                                                 ctypes.POINTER(ctypes.c_size_t),
+                                                 ctypes.POINTER(ctypes.c_size_t)]),
+    "mx_quantize_grouped_workspace": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64,
+                                                     ctypes.c_int32, ctypes.c_int64,
+                                                     ctypes.POINTER(ctypes.c_size_t)]),
+    "mx_quantize_grouped": (ctypes.c_int, [ctypes.POINTER(GroupedSourceDesc), ctypes.c_int32,
+                                           ctypes.c_int32, ctypes.c_int32, ctypes.c_uint64,
+                                           ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.c_void_p, ctypes.c_size_t,
+                                           ctypes.POINTER(GroupedDesc),
+                                           ctypes.POINTER(GroupedDesc), ctypes.c_void_p]),
+    "mx_linear_grouped": (ctypes.c_int, [ctypes.c_int32, ctypes.POINTER(GroupedDesc),
+                                         ctypes.POINTER(GroupedDesc), ctypes.c_void_p,
+                                         ctypes.POINTER(EpilogueDesc), ctypes.c_void_p,
+                                         ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p]),
     "mx_status_string": (ctypes.c_char_p, [ctypes.c_int32]),
     "mx_version": (ctypes.c_char_p, []),
     "mx_last_hip_error": (ctypes.c_char_p, []),
@@ -291,12 +365,17 @@ def _stream_handle(device, stream) -> int:
 class QTensor:
     """A quantized operand: flat uint8 buffers holding the tiled codes and
     scales (layout in include/mxfp4.h, struct mx_qtensor) plus the C
-    descriptor that points at them."""
+    descriptor that points at them. Where its source's rows belong to groups:
+    how many, and the rows of each, or -1 where the ends tell (struct
+    mx_grouped)."""
 
-    def __init__(self, codes, scales, desc: QTensorDesc):
+    def __init__(self, codes, scales, desc: QTensorDesc, groups: Optional[int] = None,
+                 group_rows: int = -1):
         self.codes = codes
         self.scales = scales
         self.desc = desc
+        self.groups = groups
+        self.group_rows = group_rows
 
     @property
     def axis(self) -> int:
@@ -806,3 +885,279 @@ def clip_grad_norm(grads, max_norm: float, out=None, stream=None):
                               norm.data_ptr(), work.data_ptr(), size, handle)
     _check(st, "mx_grad_clip")
     return norm
+
+
+@functools.lru_cache(maxsize=256)
+def quantize_grouped_sizes(rows: int, cols: int, groups: int, group_rows: int = -1,
+                           axis: int = AXIS_GROUPED) -> Tuple[int, int]:
+    """Bytes of (codes, scales) of an operand of grouped rows: axis 1, or
+    AXIS_GROUPED (see mx_quantize_grouped_sizes)."""
+    cb, sb = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(load_library().mx_quantize_grouped_sizes(rows, cols, groups, group_rows, axis, cb, sb),
+           "mx_quantize_grouped_sizes")
+    return cb.value, sb.value
+
+
+@functools.lru_cache(maxsize=256)
+def _grouped_workspace(rows: int, cols: int, groups: int, group_rows: int) -> int:
+    need = ctypes.c_size_t()
+    _check(load_library().mx_quantize_grouped_workspace(rows, cols, groups, group_rows, need),
+           "mx_quantize_grouped_workspace")
+    return need.value
+
+
+def packed_operand(codes, scales, rows: int, cols: int, axis: int, rotate: str = "hadamard",
+                   round: str = "rne", seed: int = 0, format: str = "fp4_e2m1",
+                   groups: Optional[int] = None, group_rows: int = -1) -> QTensor:
+    """The operand in existing buffers, as the quantizers laid them out (copied,
+    stored and loaded again, received from another process). rows, cols, axis
+    and the rest are those it was quantized with; with groups, axis 0 is the
+    grouped operand of quantize_grouped."""
+    import torch
+    if groups is None:
+        sizes = quantize_fp8_sizes if FORMATS[format] else quantize_sizes
+        cb, sb = sizes(rows, cols, axis)
+    else:
+        if FORMATS[format]:
+            raise ValueError("operands of grouped rows are MXFP4")
+        if axis not in (0, 1):
+            raise ValueError("axis must be 0 or 1")
+        axis = axis or AXIS_GROUPED
+        cb, sb = quantize_grouped_sizes(rows, cols, groups, group_rows, axis)
+    for t, need in ((codes, cb), (scales, sb)):
+        if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() < need:
+            raise ValueError("codes / scales must be contiguous uint8 buffers of the operand's size")
+        if not t.is_cuda or t.device != codes.device:
+            raise ValueError("codes and scales must be CUDA (HIP) tensors of one device")
+    desc = QTensorDesc(codes.data_ptr() if cb else None, scales.data_ptr() if sb else None, rows,
+                       cols, axis, 32, ROTATE[rotate], ROUND[round], seed & 0xFFFFFFFFFFFFFFFF,
+                       FORMATS[format])
+    return QTensor(codes, scales, desc, groups, group_rows)
+
+
+class GroupedQuantized(NamedTuple):
+    """What quantize_grouped returns: the axis-1 operand of the rows, the grouped
+    axis-0 operand (None without dual) and the groups' column sums (None unless
+    asked for)."""
+    q1: QTensor
+    q0: Optional[QTensor]
+    sums: object
+
+
+def _ends(ends, groups: Optional[int], device):
+    """(address, groups) of the groups' ends."""
+    import torch
+    if ends.dim() != 1 or ends.dtype != torch.int32 or ends.device != device:
+        raise ValueError("ends must be a 1-D int32 tensor on the rows' device")
+    n = ends.shape[0]
+    if n > 1 and ends.stride(0) != 1:
+        raise ValueError("ends must be contiguous")
+    if groups is not None and n != groups:
+        raise ValueError("ends and the operands differ in their number of groups")
+    return (ends.data_ptr() if n else None), n
+
+
+def quantize_grouped(x, ends=None, index=None, dual: bool = True, rotate: str = "hadamard",
+                     round: str = "rne", seed1: int = 0, seed0: int = 0, sums: bool = False,
+                     stream=None) -> GroupedQuantized:
+    """Quantize rows that belong to groups, for linear_grouped (see
+    mx_quantize_grouped).
+
+    x: 2-D bf16 CUDA rows with ends, the int32 CUDA tensor [groups] of the rows
+    behind each group's last (a running sum of the groups' sizes); or 3-D
+    [groups, rows, cols], the experts' stacked matrices, without ends. index:
+    int32 or int64 [rows], row i is then x[index[i]] (2-D x only; -1 gives zeros).
+    dual: also the axis-0 operand, in which every group's rows begin a slice of
+    their own. sums: also each group's column sums, fp32 [groups, cols]. Nothing
+    waits for the GPU. stream: as for rmsnorm_quantize.
+    """
+    import torch
+    lib = _lib or load_library()
+    if x.dtype != torch.bfloat16 or x.dim() not in (2, 3):
+        raise ValueError("x must be a 2-D or 3-D bfloat16 tensor")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA (HIP) tensor; there is no CPU path")
+    device, each, ep = x.device, -1, None
+    if x.dim() == 3:
+        if ends is not None or index is not None:
+            raise ValueError("stacked matrices take neither ends nor an index")
+        groups, each, _ = x.shape
+        if groups < 1:
+            raise ValueError("x must hold at least one matrix")
+        if x.numel() and groups > 1 and x.stride(0) != each * x.stride(1) and each > 1:
+            raise ValueError("stacked matrices must follow one another")
+        if x.numel() and each == 1:
+            x = x[:, 0]
+        else:
+            x = x.as_strided((groups * each, x.shape[2]), x.stride()[1:])
+    else:
+        if ends is None:
+            raise ValueError("rows need the ends of their groups")
+        ep, groups = _ends(ends, None, device)
+    src, cols, ld = _source_extents(x)
+    rows, ip, bits = src, None, 0
+    if index is not None:
+        if index.dim() != 1 or index.dtype not in (torch.int32, torch.int64):
+            raise ValueError("index must be a 1-D int32 or int64 tensor")
+        if index.device != device or (index.shape[0] > 1 and index.stride(0) != 1):
+            raise ValueError("index must be contiguous, on the rows' device")
+        rows, ip = index.shape[0], index.data_ptr() if index.shape[0] else None
+        bits = 64 if index.dtype == torch.int64 else 32
+        if rows == 0:
+            src, ip = 0, None
+    place, handle = _place(device, stream)
+    with place:
+        size = quantize_grouped_sizes(rows, cols, groups, each, 1)
+        if dual:
+            size += quantize_grouped_sizes(rows, cols, groups, each, AXIS_GROUPED)
+        need = _grouped_workspace(rows, cols, groups, each) if sums else 0
+        buf = [torch.empty(b, dtype=torch.uint8, device=device) for b in size]
+        ptr = [b.data_ptr() or None for b in buf] + [None, None]
+        total = torch.empty((groups, cols), dtype=torch.float32, device=device) if sums else None
+        work = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        source = GroupedSourceDesc(x.data_ptr() or None, src, cols, ld, ip, bits, rows, groups,
+                                   each, ep)
+        d1, d0 = GroupedDesc(), GroupedDesc()
+        st = lib.mx_quantize_grouped(source, 32, ROTATE[rotate], ROUND[round],
+                                     seed1 & 0xFFFFFFFFFFFFFFFF, seed0 & 0xFFFFFFFFFFFFFFFF,
+                                     ptr[0], ptr[1], ptr[2], ptr[3],
+                                     (total.data_ptr() or None) if sums else None,
+                                     work.data_ptr() if need else None, need, d1, d0, handle)
+    _check(st, "mx_quantize_grouped")
+    q1 = QTensor(buf[0], buf[1], d1.q, groups, each)
+    if not dual:
+        return GroupedQuantized(q1, None, total)
+    if not (rows and cols):     # empty operands have no buffers to tell the call by
+        d0.q = QTensorDesc(None, None, rows, cols, AXIS_GROUPED, 32, ROTATE[rotate], ROUND[round],
+                           seed0 & 0xFFFFFFFFFFFFFFFF, FORMATS["fp4_e2m1"])
+    return GroupedQuantized(q1, QTensor(buf[2], buf[3], d0.q, groups, each), total)
+
+
+def _matrix(t, name: str, shape, dtype, device):
+    """(address, leading dimension) of a matrix of an epilogue, None: none. A
+    3-D one (a matrix per group) is its rows one after another."""
+    if t is None:
+        return None, 0
+    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must have the output's type, shape and device")
+    if t.numel() == 0:
+        return None, shape[-1]
+    rows, cols = t.shape[-2:]
+    if t.stride(-1) != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    if len(shape) == 3 and shape[0] > 1:
+        if rows > 1 and t.stride(0) != rows * t.stride(1):
+            raise ValueError(f"the matrices of {name} must follow one another")
+        return t.data_ptr(), t.stride(1) if rows > 1 else t.stride(0)
+    return t.data_ptr(), t.stride(-2) if rows > 1 else max(cols, 8 * ((cols + 7) // 8))
+
+
+def _product(call: str, op: str, A: QTensor, B: QTensor, ends, out_dtype: str, activation: str,
+             bias=None, mul=None, residual=None, pre=None, grad: bool = False, dmul=None, out=None,
+             stream=None):
+    """A product with an epilogue: (C, pre or None, dmul or None). pre: the
+    matrix, or whether one is wanted (forward)."""
+    import torch
+    lib = _lib or load_library()
+    dtype = {"f32": torch.float32, "bf16": torch.bfloat16}[out_dtype]
+    device = A.codes.device
+    if B.codes.device != device:
+        raise ValueError("the operands are on different devices")
+    bias_shape = ()
+    if ends is None:
+        shape = (A.mn, B.mn)
+        for q in (A, B):
+            if q.desc.axis == AXIS_GROUPED:
+                raise ValueError("a grouped operand needs the ends of its groups")
+    else:
+        if B.groups is None:
+            raise ValueError("B must be an operand of grouped rows")
+        ep, groups = _ends(ends, B.groups, device)
+        bias_shape = (groups,)
+        shape = ((groups, A.mn, B.mn) if op == "wgrad"
+                 else (A.mn, B.group_rows if op == "fprop" else B.mn))
+    n = shape[-1]
+    bp, bias_dtype = None, 0
+    if bias is not None:
+        if tuple(bias.shape) != bias_shape + (n,) or bias.device != device:
+            raise ValueError("bias must have a value for each column (of each group)")
+        if not bias.is_contiguous():
+            raise ValueError("bias must be contiguous")
+        bias_dtype, bp = _row_dtype(bias, "bias"), bias.data_ptr() or None
+    mp, ldmul = _matrix(mul, "mul", shape, dtype, device)
+    rp, ldres = _matrix(residual, "residual", shape, dtype, device)
+    place, handle = _place(device, stream)
+    with place:
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=device)
+        cp, ldc = _matrix(out, "out", shape, dtype, device)
+        if pre is True:
+            pre = torch.empty(shape, dtype=dtype, device=device)
+        pre = None if pre is False else pre
+        pp, ldpre = _matrix(pre, "pre", shape, dtype, device)
+        if grad and mul is not None and dmul is None:
+            dmul = torch.empty(shape, dtype=dtype, device=device)
+        dp, lddmul = _matrix(dmul, "dmul", shape, dtype, device)
+        e = EpilogueDesc(ACTIVATIONS[activation], int(grad), bp, bias_dtype, mp, rp, pp, dp, ldmul,
+                         ldres, ldpre, lddmul)
+        if ends is None:
+            st = lib.mx_linear_fused(OPS[op], A.desc, B.desc, e, cp, ldc, OUT_DTYPES[out_dtype],
+                                     handle)
+        else:
+            da = GroupedDesc(A.desc, A.groups if A.groups is not None else groups, A.group_rows)
+            st = lib.mx_linear_grouped(OPS[op], da, GroupedDesc(B.desc, B.groups, B.group_rows),
+                                       ep, e, cp, ldc, OUT_DTYPES[out_dtype], handle)
+    _check(st, call)
+    return out, pre, dmul
+
+
+def linear_fused(op: str, A: QTensor, B: QTensor, out_dtype: str = "f32", bias=None,
+                 activation: str = "none", mul=None, residual=None, save_pre=False, out=None,
+                 stream=None):
+    """act(A B^T + bias) * mul + residual, one launch (see mx_linear_fused).
+
+    op, A, B, out: as for linear (MXFP4 operands). bias: fp32 or bf16 [N].
+    activation: one of ACTIVATIONS. mul, residual: matrices of the output's type
+    and shape (row-strided views allowed); either may be out itself, so
+    residual=out, out=out adds onto it. save_pre: also return A B^T + bias, in
+    the output's type, for linear_act_backward (True, or the matrix to write):
+    (C, pre) instead of C. stream: as for rmsnorm_quantize.
+    """
+    c, pre, _ = _product("mx_linear_fused", op, A, B, None, out_dtype, activation, bias, mul,
+                         residual, save_pre, out=out, stream=stream)
+    return c if save_pre is False else (c, pre)
+
+
+def linear_act_backward(A: QTensor, B: QTensor, pre, activation: str, mul=None, ends=None,
+                        out_dtype: str = "f32", out=None, dmul=None, stream=None):
+    """The gradient of act(pre) * mul taken back through the gate and the
+    activation in the epilogue of the product that computes it (see
+    mx_linear_fused): with g = linear("dgrad", A, B), returns g * mul *
+    act'(pre), the gradient of pre; with mul the pair of it and g * act(pre), the
+    gradient of mul. A: q(dY), axis 1; B: q(W), axis 0. With ends (and B from
+    quantize_grouped) over experts, as linear_grouped. out may be pre or mul
+    itself, dmul too.
+    """
+    call = "mx_linear_fused" if ends is None else "mx_linear_grouped"
+    c, _, dmul = _product(call, "dgrad", A, B, ends, out_dtype, activation, mul=mul, pre=pre,
+                          grad=True, dmul=dmul, out=out, stream=stream)
+    return c if mul is None else (c, dmul)
+
+
+def linear_grouped(op: str, A: QTensor, B: QTensor, ends, out_dtype: str = "f32", bias=None,
+                   activation: str = "none", mul=None, residual=None, save_pre=False, out=None,
+                   stream=None):
+    """linear_fused with one matrix per group of rows (the experts of a layer), in
+    one launch (see mx_linear_grouped).
+
+    fprop: A = q(X) [T, in] axis 1 (quantize_grouped, quantize or
+    rmsnorm_quantize), B = quantize_grouped(W [groups, out, in]).q1 -> [T, out].
+    dgrad: A = q(dY) axis 1, B = quantize_grouped(W).q0 -> [T, in]. wgrad: A, B =
+    the q0 of quantize_grouped(dY, ends) and quantize_grouped(X, ends) ->
+    [groups, out, in]. ends: int32 [groups], the row behind each group's last;
+    rows behind the last end are left as they were in out and pre. bias: [groups,
+    N]. The rest as for linear_fused.
+    """
+    c, pre, _ = _product("mx_linear_grouped", op, A, B, ends, out_dtype, activation, bias, mul,
+                         residual, save_pre, out=out, stream=stream)
+    return c if save_pre is False else (c, pre)

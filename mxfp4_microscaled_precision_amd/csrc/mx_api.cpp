@@ -820,6 +820,307 @@ mx_status mx_grad_clip(const mx_grad_set *in, const mx_grad_set *out, float max_
                                          static_cast<hipStream_t>(stream)));
 }
 
+namespace {
+
+constexpr int32_t kMaxGroups = 65536;
+
+// 128-deep slices of a grouped axis-0 operand.
+static int64_t grouped_slices(int64_t rows, int32_t groups, int64_t group_rows) {
+  return group_rows >= 0 ? (int64_t)groups * ((group_rows + 127) / 128)
+                         : (rows + 127 * (int64_t)groups) / 128;
+}
+
+static mx_status check_groups(int64_t rows, int32_t groups, int64_t group_rows) {
+  if (groups < 1 || group_rows < -1) return MX_ERR_ARG;
+  if (rows < 0) return MX_ERR_SHAPE;
+  if (groups > kMaxGroups || rows > kMaxExtent || group_rows > kMaxExtent)
+    return MX_ERR_UNSUPPORTED;
+  if (group_rows >= 0 && rows != groups * group_rows) return MX_ERR_SHAPE;
+  return MX_OK;
+}
+
+// Padded extents of an operand of grouped rows (empty ones stay empty).
+static void grouped_extents(int64_t rows, int64_t cols, int32_t groups, int64_t group_rows,
+                            int32_t axis, int64_t *mnp, int64_t *kp) {
+  if (axis == 1) {
+    padded_extents(rows, cols, 1, mnp, kp);
+    return;
+  }
+  const bool empty = rows == 0 || cols == 0;
+  *mnp = empty ? 0 : (cols + 255) / 256 * 256;
+  *kp = empty ? 0 : 128 * grouped_slices(rows, groups, group_rows);
+}
+
+static mx_status grouped_sizes(int64_t rows, int64_t cols, int32_t groups, int64_t group_rows,
+                               int32_t axis, size_t *codes_bytes, size_t *scales_bytes) {
+  if (codes_bytes == nullptr || scales_bytes == nullptr) return MX_ERR_NULL;
+  if (axis != 1 && axis != MX_AXIS_GROUPED) return MX_ERR_ARG;
+  const mx_status st = check_groups(rows, groups, group_rows);
+  if (st != MX_OK) return st;
+  if (cols < 0 || cols % 32 != 0) return MX_ERR_SHAPE;
+  if (cols > kMaxExtent) return MX_ERR_UNSUPPORTED;
+  int64_t mnp, kp;
+  grouped_extents(rows, cols, groups, group_rows, axis, &mnp, &kp);
+  *codes_bytes = (size_t)mnp * (size_t)kp / 2;
+  *scales_bytes = (size_t)mnp * (size_t)kp / 32;
+  return MX_OK;
+}
+
+// Operand of a grouped product: ragged or equal groups along its rows.
+static mx_status check_grouped(const mx_grouped *g, int32_t axis, bool ragged) {
+  if (g == nullptr) return MX_ERR_NULL;
+  const mx_qtensor &q = g->q;
+  if (q.axis != axis || (g->group_rows == -1) != ragged || q.block != 32) return MX_ERR_ARG;
+  if (!valid_rotate(q.rotate) || !valid_round(q.round) || !valid_format(q.format))
+    return MX_ERR_ARG;
+  const mx_status st = check_groups(q.rows, g->groups, g->group_rows);
+  if (st != MX_OK) return st;
+  if (q.format != MX_FMT_FP4_E2M1) return MX_ERR_UNSUPPORTED;
+  if (q.cols < 0 || (axis == 1 && q.cols % 32 != 0)) return MX_ERR_SHAPE;
+  if (q.rows == 0 || q.cols == 0) return MX_OK;
+  if (q.codes == nullptr || q.scales == nullptr) return MX_ERR_NULL;
+  if (!aligned(q.codes, 16) || !aligned(q.scales, 4)) return MX_ERR_ALIGN;
+  if (extents_too_large(q.rows, q.cols)) return MX_ERR_UNSUPPORTED;
+  int64_t mnp, kp;
+  grouped_extents(q.rows, q.cols, g->groups, g->group_rows, axis, &mnp, &kp);
+  if (mnp * kp / 2 >= kMaxCodeBytes) return MX_ERR_UNSUPPORTED;
+  return MX_OK;
+}
+
+// One matrix of an epilogue: C's type, `rows` rows of N.
+static mx_status check_matrix(const void *p, int64_t rows, int64_t N, int64_t ld, int32_t dtype) {
+  if (p == nullptr) return MX_OK;
+  if (ld < N) return MX_ERR_SHAPE;
+  if (!aligned(p, dtype_size(dtype))) return MX_ERR_ALIGN;
+  if (span_too_large(rows, ld, dtype_size(dtype))) return MX_ERR_UNSUPPORTED;
+  return MX_OK;
+}
+
+// The epilogue's checks and arguments for a C [rows][N].
+static mx_status fill_epilogue(const mx_epilogue *e, void *C, int64_t rows, int64_t N, int64_t ldc,
+                               int32_t dtype, mx::FusedArgs *g) {
+  const mx_epilogue none = {};
+  if (e == nullptr) e = &none;
+  if (e->activation < MX_ACT_NONE || e->activation > MX_ACT_GELU_TANH) return MX_ERR_ARG;
+  if (e->gradient != 0 && e->gradient != 1) return MX_ERR_ARG;
+  if (e->bias != nullptr && !valid_dtype(e->bias_dtype)) return MX_ERR_ARG;
+  const bool grad = e->gradient == 1;
+  if (grad && (e->bias != nullptr || e->residual != nullptr)) return MX_ERR_ARG;
+  if (e->dmul != nullptr && (!grad || e->mul == nullptr)) return MX_ERR_ARG;
+  const bool empty = rows == 0 || N == 0;
+  if (grad && e->pre == nullptr && !empty) return MX_ERR_NULL;
+  struct Matrix { const void *p; int64_t ld; bool out; };
+  const Matrix m[5] = {{C, ldc, true}, {e->mul, e->ldmul, false}, {e->residual, e->ldres, false},
+                       {e->pre, e->ldpre, !grad}, {e->dmul, e->lddmul, true}};
+  int vec = 1;
+  for (int i = 0; i < 5; ++i) {
+    const mx_status st = empty ? MX_OK : check_matrix(m[i].p, rows, N, m[i].ld, dtype);
+    if (st != MX_OK) return st;
+    if (m[i].p == nullptr) continue;
+    if (!aligned(m[i].p, 16) || m[i].ld * dtype_size(dtype) % 16 != 0) vec = 0;
+    for (int j = 0; j < i && !empty; ++j) {
+      if (m[j].p != m[i].p) continue;
+      if (m[i].out && m[j].out) return MX_ERR_ARG;
+      if (m[i].ld != m[j].ld && (m[i].out || m[j].out)) return MX_ERR_SHAPE;
+    }
+  }
+  if (e->bias != nullptr && !aligned(e->bias, dtype_size(e->bias_dtype))) return MX_ERR_ALIGN;
+  g->c = C;
+  g->ldc = ldc;
+  g->out_bf16 = dtype == MX_OUT_BF16 ? 1 : 0;
+  g->grad = grad ? 1 : 0;
+  g->e = mx::EpiArgs{e->bias, e->mul, e->residual, e->pre, e->dmul, e->ldmul, e->ldres, e->ldpre,
+                     e->lddmul, e->bias_dtype == MX_OUT_F32 ? 1 : 0, e->activation, vec};
+  return MX_OK;
+}
+
+static void fill_operands(const mx_qtensor *A, const mx_qtensor *B, mx::FusedArgs *g) {
+  g->a_codes = static_cast<const uint8_t *>(A->codes);
+  g->a_scales = static_cast<const uint8_t *>(A->scales);
+  g->b_codes = static_cast<const uint8_t *>(B->codes);
+  g->b_scales = static_cast<const uint8_t *>(B->scales);
+}
+
+static bool rotations_match(const mx_qtensor *A, const mx_qtensor *B) {
+  return A->rotate == B->rotate &&
+         (A->rotate != MX_ROT_RAND_SIGN_HADAMARD || (uint32_t)A->seed == (uint32_t)B->seed);
+}
+
+}  // namespace
+
+mx_status mx_linear_fused(int32_t op, const mx_qtensor *A, const mx_qtensor *B,
+                          const mx_epilogue *epilogue, void *C, int64_t ldc, int32_t out_dtype,
+                          void *stream) {
+  mx::GemmArgs d;
+  bool empty = false;
+  mx_status st = linear_entry(op, A, B, C, ldc, out_dtype, &d, &empty);
+  if (st != MX_OK) return st;
+  if (A->format != MX_FMT_FP4_E2M1) return MX_ERR_UNSUPPORTED;
+  mx::FusedArgs g = {};
+  st = fill_epilogue(epilogue, C, d.M, d.N, ldc, out_dtype, &g);
+  if (st != MX_OK || empty) return st;
+  if (d.M > INT32_MAX - 256 || d.N > INT32_MAX - 256) return MX_ERR_UNSUPPORTED;
+  fill_operands(A, B, &g);
+  g.kind = mx::MX_K_FPROP;
+  g.groups = 1;
+  g.ends = nullptr;
+  g.rows = g.M = (int)d.M;
+  g.N = (int)d.N;
+  g.a_panels = (int)((d.M + 255) / 256);
+  g.b_panels = (int)((d.N + 255) / 256);
+  g.a_slices = g.b_slices = (int)((d.K + 127) / 128);
+  return hip_status(mx::fused_launch(g, static_cast<hipStream_t>(stream)));
+}
+
+mx_status mx_quantize_grouped_sizes(int64_t rows, int64_t cols, int32_t groups,
+                                    int64_t group_rows, int32_t axis, size_t *codes_bytes,
+                                    size_t *scales_bytes) {
+  return grouped_sizes(rows, cols, groups, group_rows, axis, codes_bytes, scales_bytes);
+}
+
+mx_status mx_quantize_grouped_workspace(int64_t rows, int64_t cols, int32_t groups,
+                                        int64_t group_rows, size_t *bytes) {
+  if (bytes == nullptr) return MX_ERR_NULL;
+  size_t c, s;
+  const mx_status st =
+      grouped_sizes(rows, cols, groups, group_rows, MX_AXIS_GROUPED, &c, &s);
+  if (st != MX_OK) return st;
+  // a row of partial sums per 32-deep block
+  *bytes = rows == 0 ? 0 : (size_t)grouped_slices(rows, groups, group_rows) * 4 * (size_t)cols * 4;
+  return MX_OK;
+}
+
+mx_status mx_quantize_grouped(const mx_grouped_source *source, int32_t block, int32_t rotate,
+                              int32_t round, uint64_t seed1, uint64_t seed0, void *codes1,
+                              void *scales1, void *codes0, void *scales0, float *sums,
+                              void *workspace, size_t workspace_bytes, mx_grouped *desc1,
+                              mx_grouped *desc0, void *stream) {
+  if (source == nullptr) return MX_ERR_NULL;
+  const mx_grouped_source &x = *source;
+  if (block != 32) return MX_ERR_ARG;
+  if (!valid_rotate(rotate) || !valid_round(round)) return MX_ERR_ARG;
+  mx_status st = check_groups(x.rows, x.groups, x.group_rows);
+  if (st != MX_OK) return st;
+  if (x.cols < 0 || x.src_rows < 0 || x.cols % 32 != 0) return MX_ERR_SHAPE;
+  if (x.index == nullptr ? x.src_rows != x.rows : false) return MX_ERR_SHAPE;
+  if (x.index != nullptr && x.index_bits != 32 && x.index_bits != 64) return MX_ERR_ARG;
+  const bool dual = codes0 != nullptr || scales0 != nullptr;
+  const bool empty = x.rows == 0 || x.cols == 0;
+  size_t need = 0;
+  if (x.cols > kMaxExtent || x.src_rows > kMaxExtent) return MX_ERR_UNSUPPORTED;
+  if (!empty) {
+    if ((x.x == nullptr && x.src_rows > 0) || codes1 == nullptr || scales1 == nullptr ||
+        (dual && (codes0 == nullptr || scales0 == nullptr)))
+      return MX_ERR_NULL;
+    if (x.ld < x.cols) return MX_ERR_SHAPE;
+    if (!aligned(x.x, 16) || x.ld % 8 != 0 || !aligned(codes1, 16) || !aligned(scales1, 4) ||
+        (dual && (!aligned(codes0, 16) || !aligned(scales0, 4))))
+      return MX_ERR_ALIGN;
+    if (x.index != nullptr && !aligned(x.index, x.index_bits / 8)) return MX_ERR_ALIGN;
+    if (span_too_large(x.src_rows, x.ld, 2)) return MX_ERR_UNSUPPORTED;
+    for (int32_t axis = 1; axis <= MX_AXIS_GROUPED; ++axis) {
+      int64_t mnp, kp;
+      grouped_extents(x.rows, x.cols, x.groups, x.group_rows, axis, &mnp, &kp);
+      if (mnp * kp / 2 >= kMaxCodeBytes) return MX_ERR_UNSUPPORTED;
+    }
+  }
+  if (x.group_rows == -1 && !(x.cols == 0)) {
+    if (x.ends == nullptr) return MX_ERR_NULL;
+    if (!aligned(x.ends, 4)) return MX_ERR_ALIGN;
+  }
+  if (sums != nullptr) {
+    st = mx_quantize_grouped_workspace(x.rows, x.cols, x.groups, x.group_rows, &need);
+    if (st != MX_OK) return st;
+    if (!aligned(sums, 4) || !aligned(workspace, 16)) return MX_ERR_ALIGN;
+    if (need > 0 && workspace == nullptr) return MX_ERR_NULL;
+    if (workspace_bytes < need) return MX_ERR_SHAPE;
+  }
+  if (desc1 != nullptr) {
+    fill_desc(&desc1->q, codes1, scales1, x.rows, x.cols, 1, block, rotate, round, seed1,
+              MX_FMT_FP4_E2M1);
+    desc1->groups = x.groups;
+    desc1->group_rows = x.group_rows;
+  }
+  if (dual && desc0 != nullptr) {
+    fill_desc(&desc0->q, codes0, scales0, x.rows, x.cols, MX_AXIS_GROUPED, block, rotate, round,
+              seed0, MX_FMT_FP4_E2M1);
+    desc0->groups = x.groups;
+    desc0->group_rows = x.group_rows;
+  }
+  if (x.cols == 0 || (x.rows == 0 && sums == nullptr)) return MX_OK;
+  mx::GroupedQuantArgs a = {};
+  a.x = static_cast<const uint16_t *>(x.x);
+  a.index = x.index;
+  a.ends = x.group_rows == -1 ? x.ends : nullptr;
+  a.src_rows = x.src_rows;
+  a.cols = x.cols;
+  a.ld = x.ld;
+  a.rows = (int)x.rows;
+  a.groups = x.groups;
+  a.each = x.group_rows == -1 ? 0 : (int)x.group_rows;
+  a.index64 = x.index_bits == 64 ? 1 : 0;
+  a.slices = (int)grouped_slices(x.rows, x.groups, x.group_rows);
+  a.rotate = rotate;
+  a.round = round;
+  a.seed1_lo = (uint32_t)(seed1 & 0xFFFFFFFFull);
+  a.seed1_hi = (uint32_t)(seed1 >> 32);
+  a.seed0_lo = (uint32_t)(seed0 & 0xFFFFFFFFull);
+  a.seed0_hi = (uint32_t)(seed0 >> 32);
+  a.codes1 = static_cast<uint8_t *>(codes1);
+  a.scales1 = static_cast<uint8_t *>(scales1);
+  a.codes0 = static_cast<uint8_t *>(codes0);
+  a.scales0 = static_cast<uint8_t *>(scales0);
+  a.partial = sums != nullptr ? static_cast<float *>(workspace) : nullptr;
+  a.sums = sums;
+  return hip_status(mx::quantize_grouped_launch(a, static_cast<hipStream_t>(stream)));
+}
+
+mx_status mx_linear_grouped(int32_t op, const mx_grouped *A, const mx_grouped *B,
+                            const int32_t *ends, const mx_epilogue *epilogue, void *C,
+                            int64_t ldc, int32_t out_dtype, void *stream) {
+  if (op != MX_OP_FPROP && op != MX_OP_DGRAD && op != MX_OP_WGRAD) return MX_ERR_ARG;
+  if (!valid_dtype(out_dtype)) return MX_ERR_ARG;
+  const bool wgrad = op == MX_OP_WGRAD;
+  mx_status st = check_grouped(A, wgrad ? MX_AXIS_GROUPED : 1, true);
+  if (st != MX_OK) return st;
+  st = check_grouped(B, op == MX_OP_FPROP ? 1 : MX_AXIS_GROUPED, wgrad);
+  if (st != MX_OK) return st;
+  if (!rotations_match(&A->q, &B->q)) return MX_ERR_MISMATCH;
+  if (A->groups != B->groups) return MX_ERR_SHAPE;
+  // A's and B's reduction extents
+  if (op == MX_OP_FPROP ? A->q.cols != B->q.cols
+                        : op == MX_OP_DGRAD ? A->q.cols != B->group_rows : A->q.rows != B->q.rows)
+    return MX_ERR_SHAPE;
+  const int64_t M = wgrad ? A->q.cols : A->q.rows;
+  const int64_t N = op == MX_OP_FPROP ? B->group_rows : B->q.cols;
+  const int64_t c_rows = wgrad ? M * A->groups : M;
+  if (ldc < N) return MX_ERR_SHAPE;
+  const bool empty = M == 0 || N == 0;
+  if (!empty) {
+    if (C == nullptr || ends == nullptr) return MX_ERR_NULL;
+    if (!aligned(ends, 4)) return MX_ERR_ALIGN;
+    if (M > INT32_MAX - 256 || N > INT32_MAX - 256) return MX_ERR_UNSUPPORTED;
+  }
+  mx::FusedArgs g = {};
+  st = fill_epilogue(epilogue, C, c_rows, N, ldc, out_dtype, &g);
+  if (st != MX_OK || empty) return st;
+  fill_operands(&A->q, &B->q, &g);
+  g.kind = op;
+  g.groups = A->groups;
+  g.ends = ends;
+  g.rows = (int)A->q.rows;
+  g.M = (int)M;
+  g.N = (int)N;
+  int64_t mnp, kp;
+  grouped_extents(A->q.rows, A->q.cols, A->groups, A->group_rows, A->q.axis, &mnp, &kp);
+  g.a_panels = (int)(mnp / 256);
+  g.a_slices = (int)(kp / 128);
+  grouped_extents(B->q.rows, B->q.cols, B->groups, B->group_rows, B->q.axis, &mnp, &kp);
+  g.b_panels = (int)(mnp / 256);
+  g.b_slices = (int)(kp / 128);
+  return hip_status(mx::fused_launch(g, static_cast<hipStream_t>(stream)));
+}
+
 const char *mx_status_string(int32_t status) {
   switch (status) {
     case MX_OK: return "MX_OK";

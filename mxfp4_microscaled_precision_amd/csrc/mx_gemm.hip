@@ -35,19 +35,6 @@ using namespace gemm;
 
 typedef double d2 __attribute__((ext_vector_type(2)));
 
-constexpr int kFmtFp4 = 4;
-
-// One 16x16x128 FP4 MFMA. The E8M0 scale of each operand is byte SELA / SELB
-// of the given register (the instruction's byte select).
-template <int SELA, int SELB>
-__device__ __forceinline__ v4f mfma_fp4(const uint4 &a, const uint4 &b, v4f c, uint32_t sa,
-                                        uint32_t sb) {
-  const v8i av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
-  const v8i bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, kFmtFp4, kFmtFp4, SELA,
-                                                          (int)sa, SELB, (int)sb);
-}
-
 // Entry e of a grouped launch, one field at a time (e is wave-uniform:
 // scalar selects between fields at fixed offsets, so the kernel argument
 // block is never indexed at run time, which would copy it to scratch).

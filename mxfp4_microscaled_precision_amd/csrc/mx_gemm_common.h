@@ -85,6 +85,19 @@ __device__ __forceinline__ void dma_load16(v4i rsrc, int voffset, uint32_t lds_b
 }
 
 
+constexpr int kFmtFp4 = 4;
+
+// One 16x16x128 FP4 MFMA. The E8M0 scale of each operand is byte SELA / SELB
+// of the given register (the instruction's byte select).
+template <int SELA, int SELB>
+__device__ __forceinline__ v4f mfma_fp4(const uint4 &a, const uint4 &b, v4f c, uint32_t sa,
+                                        uint32_t sb) {
+  const v8i av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+  const v8i bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, kFmtFp4, kFmtFp4, SELA,
+                                                          (int)sa, SELB, (int)sb);
+}
+
 // Tile index -> (tile_m, tile_n): workgroups are dispatched round-robin over
 // the 8 XCDs, so consecutive ids are first regrouped per XCD, then ordered in
 // groups of kGroupM tile rows so that each XCD works on a compact 2-D region

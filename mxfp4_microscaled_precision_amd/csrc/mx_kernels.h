@@ -94,6 +94,62 @@ hipError_t gemm_e4m3_launch(const GemmArgs &g, hipStream_t stream);
 // Compute units of the current device (one persistent GEMM workgroup each).
 int cu_count();
 
+enum { MX_K_ACT_NONE = 0, MX_K_ACT_RELU = 1, MX_K_ACT_SILU = 2, MX_K_ACT_GELU = 3,
+       MX_K_ACT_GELU_TANH = 4 };
+
+// What a product's epilogue reads and writes besides C: matrices of C's type
+// and rows, null where the call has none (see mx_epilogue in mxfp4.h).
+struct EpiArgs {
+  const void *bias;                // [N], or [groups][N]
+  const void *mul, *residual;
+  void *pre;                       // written; read by a gradient
+  void *dmul;
+  int64_t ldmul, ldres, ldpre, lddmul;
+  int bias_f32, act;
+  int vec;                         // every matrix (C too) takes 16-byte accesses at columns 8 i
+};
+
+enum { MX_K_FPROP = 0, MX_K_DGRAD = 1, MX_K_WGRAD = 2 };
+
+// A product with an epilogue, of one group (dense) or of one per expert. The
+// operands are packed; C's rows are A's (fprop, dgrad) or the groups' matrices
+// one after another (wgrad).
+//   fprop  A [M][K] by rows, B [groups * N][K]: group e's rows with rows e N ..
+//   dgrad  A [M][K] by rows, B [N][groups * Kp]: with the slices of group e
+//   wgrad  A [M][..], B [N][..]: group e's slices of both, group e's C [M][N]
+struct FusedArgs {
+  const uint8_t *a_codes, *a_scales, *b_codes, *b_scales;
+  void *c;
+  int64_t ldc;
+  int kind, out_bf16, grad;
+  int groups;
+  const int32_t *ends;             // device; null: one group of all rows (dense)
+  int rows;                        // rows that `ends` is about (wgrad: summed over)
+  int M, N;
+  int a_panels, b_panels;          // 256-row panels of each operand
+  int a_slices, b_slices;          // 128-deep slices of each operand
+  EpiArgs e;
+};
+
+hipError_t fused_launch(const FusedArgs &g, hipStream_t stream);
+
+// Gathered rows in groups, quantized in both orientations, and their sums.
+struct GroupedQuantArgs {
+  const uint16_t *x;               // bf16 [src_rows, cols], leading dimension ld
+  const void *index;               // [rows] source rows, or null: row i is x's row i
+  const int32_t *ends;             // device [groups], or null: groups of `each` rows
+  int64_t src_rows, cols, ld;
+  int rows, groups, each, index64;
+  int slices;                      // 128-deep slices of the axis-0 operand
+  int rotate, round;
+  uint32_t seed1_lo, seed1_hi, seed0_lo, seed0_hi;
+  uint8_t *codes1, *scales1;
+  uint8_t *codes0, *scales0;       // or null
+  float *partial, *sums;           // [4 slices][cols], [groups][cols], or null
+};
+
+hipError_t quantize_grouped_launch(const GroupedQuantArgs &a, hipStream_t stream);
+
 // fp32 values of a packed operand in its source's shape.
 struct DequantArgs {
   const uint8_t *codes, *scales;   // tiled (E2M1 or E4M3 codes)
