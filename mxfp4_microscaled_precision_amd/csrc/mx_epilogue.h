@@ -4,13 +4,17 @@
 //   forward    z = acc + bias;  pre = z;  C = act(z) * mul + residual
 //   gradient   C = acc * mul * act'(pre);  dmul = acc * act(pre)
 //
-// A lane owns 8 columns (16 bytes of a bf16 row, 32 of an fp32 one), so mul,
-// residual, pre and C are read and written as whole 128-byte row pieces by
-// eight lanes; which activation it is is a wave-uniform branch.
+// A lane owns 8 columns of a row (16 bytes of a bf16 row, 32 of an fp32 one), so
+// mul, residual, pre and C are read and written as whole 128-byte row pieces by
+// eight lanes; where their addresses are not for 16-byte accesses the tile
+// kernel's lanes own a column of 8 rows instead, 64 lanes 64 columns. Which
+// activation it is is a wave-uniform branch.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "mx_kernels.h"
 #include "mx_rows.h"
@@ -48,7 +52,8 @@ constexpr float kGelu1 = 1.59576912f, kGelu3 = 0.0713548163f;
 
 // act(z). The limits at the infinities; NaN stays NaN. (A product with -1e30
 // in -inf's place keeps the limit 0 where the formula has -inf * 0.)
-__device__ __forceinline__ float act_value(float z, int act) {
+template <int act>
+__device__ __forceinline__ float act_value(float z) {
   if (act == MX_K_ACT_SILU) return fmaxf(z, -1e30f) * logistic(z);
   if (act == MX_K_ACT_GELU_TANH)
     return fmaxf(z, -1e30f) * logistic(z * __builtin_fmaf(kGelu3 * z, z, kGelu1));
@@ -64,7 +69,8 @@ __device__ __forceinline__ float act_value(float z, int act) {
 
 // act(z) and act'(z). Beyond +-64 the slopes are 0 and 1 in fp32, so the
 // clamp only keeps infinity * 0 away.
-__device__ __forceinline__ float act_both(float z, int act, float &slope) {
+template <int act>
+__device__ __forceinline__ float act_both(float z, float &slope) {
   const float zc = __builtin_amdgcn_fmed3f(z, -128.0f, 128.0f);
   if (act == MX_K_ACT_SILU || act == MX_K_ACT_GELU_TANH) {
     const bool tanh_form = act == MX_K_ACT_GELU_TANH;
@@ -88,106 +94,139 @@ __device__ __forceinline__ float act_both(float z, int act, float &slope) {
   return __builtin_fmaf(-fminf(fabsf(z), 64.0f), c, up);
 }
 
-// Eight elements of a [.., ld] matrix as stored (F32: fp32, else bf16).
-template <int F32>
-__device__ __forceinline__ Row8<F32> epi_load(const void *p, int64_t at, bool vec, int lo, int hi) {
-  if (vec) return load8<F32>(p, at);
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[i] = 0.0f;
-    if (i >= lo && i < hi)
-      v[i] = F32 ? static_cast<const float *>(p)[at + i]
-                 : bits_f((uint32_t) static_cast<const uint16_t *>(p)[at + i] << 16);
+// Calls f with the activation as a constant: one branch where f's elements
+// would otherwise branch each (and wait for each other's exponentials).
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f) {
+  switch (act) {
+    case MX_K_ACT_RELU: f(std::integral_constant<int, MX_K_ACT_RELU>()); break;
+    case MX_K_ACT_SILU: f(std::integral_constant<int, MX_K_ACT_SILU>()); break;
+    case MX_K_ACT_GELU: f(std::integral_constant<int, MX_K_ACT_GELU>()); break;
+    case MX_K_ACT_GELU_TANH: f(std::integral_constant<int, MX_K_ACT_GELU_TANH>()); break;
+    default: f(std::integral_constant<int, MX_K_ACT_NONE>()); break;
   }
-  return narrow8<F32>(v);
 }
 
+// The epilogue of eight elements, whose stored values of mul and of the residual
+// (of pre, for a gradient) are in `mul` and `other`: C in c, pre (dmul, for a
+// gradient) in second, as stored. Four elements at a time: enough to overlap
+// their exponentials, and little that is live besides the sums (a wave of the
+// tile kernel holds 128 of them).
+template <int F32, bool GRAD, int ACT>
+__device__ __forceinline__ void epilogue8(const float (&v)[8], const float (&bias)[8], bool has_mul,
+                                          bool has_residual, const Row8<F32> &mul,
+                                          const Row8<F32> &other, Row8<F32> &c, Row8<F32> &second) {
+  auto element = [](const Row8<F32> &r, int i) {
+    if constexpr (F32)
+      return bits_f(r.w[i >> 2][i & 3]);
+    else
+      return bits_f(i & 1 ? r.w[0][i >> 1] & 0xFFFF0000u : r.w[0][i >> 1] << 16);
+  };
+  auto put = [](Row8<F32> &r, int i, const float (&x)[4]) {      // elements i .. i + 3
+#pragma unroll
+    for (int k = 0; k < 4; k += F32 ? 1 : 2) {
+      if constexpr (F32) {
+        r.w[i >> 2][k] = f_bits(x[k]);
+      } else {
+        typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+        typedef float f2 __attribute__((ext_vector_type(2)));
+        r.w[0][(i + k) >> 1] =
+            __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{x[k], x[k + 1]}), bf2));
+      }
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < 8; i += 4) {
+    float a[4], b[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (GRAD) {
+        float slope;
+        b[k] = v[i + k] * act_both<ACT>(element(other, i + k), slope);
+        a[k] = v[i + k] * slope;
+      } else {
+        b[k] = v[i + k] + bias[i + k];
+        a[k] = act_value<ACT>(b[k]);
+      }
+    }
+    put(second, i, b);
+    if (has_mul) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) a[k] *= element(mul, i + k);
+    }
+    if (!GRAD && has_residual) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) a[k] += element(other, i + k);
+    }
+    put(c, i, a);
+  }
+}
+
+// The second output, and what `other` is read from.
+template <bool GRAD>
+__device__ __forceinline__ void *second_of(const EpiArgs &e) {
+  return GRAD ? e.dmul : e.pre;
+}
+template <bool GRAD>
+__device__ __forceinline__ int64_t second_ld(const EpiArgs &e) {
+  return GRAD ? e.lddmul : e.ldpre;
+}
+template <bool GRAD>
+__device__ __forceinline__ const void *other_of(const EpiArgs &e) {
+  return GRAD ? e.pre : e.residual;
+}
+template <bool GRAD>
+__device__ __forceinline__ int64_t other_ld(const EpiArgs &e) {
+  return GRAD ? e.ldpre : e.ldres;
+}
+
+// One element as stored, into element i of eight, and back.
 template <int F32>
-__device__ __forceinline__ void epi_store(void *p, int64_t at, bool vec, int lo, int hi,
-                                          const float (&v)[8]) {
-  const Row8<F32> r = narrow8<F32>(v);
+__device__ __forceinline__ uint32_t load_bits(const void *p, int64_t at) {
+  return F32 ? static_cast<const uint32_t *>(p)[at] : static_cast<const uint16_t *>(p)[at];
+}
+template <int F32>
+__device__ __forceinline__ void put_bits(Row8<F32> &r, int i, uint32_t bits) {
+  if constexpr (F32)
+    r.w[i >> 2][i & 3] = bits;
+  else
+    r.w[0][i >> 1] = i & 1 ? r.w[0][i >> 1] | bits << 16 : bits;      // even elements first
+}
+template <int F32>
+__device__ __forceinline__ void store_bits(void *p, int64_t at, const Row8<F32> &r, int i) {
+  if constexpr (F32)
+    static_cast<uint32_t *>(p)[at] = r.w[i >> 2][i & 3];
+  else
+    static_cast<uint16_t *>(p)[at] = (uint16_t)(r.w[0][i >> 1] >> (16 * (i & 1)));
+}
+
+// Bias of one column (element `at` of all groups' biases).
+__device__ __forceinline__ float load_bias(const EpiArgs &e, int64_t at) {
+  return e.bias_f32 ? static_cast<const float *>(e.bias)[at]
+                    : bits_f((uint32_t) static_cast<const uint16_t *>(e.bias)[at] << 16);
+}
+
+// Eight consecutive columns of a row, from element `at` on: `vec` as one
+// access, else those in [lo, hi) one by one.
+template <int F32>
+__device__ __forceinline__ Row8<F32> load_cols(const void *p, int64_t at, bool vec, int lo,
+                                               int hi) {
+  if (vec) return load8<F32>(p, at);
+  Row8<F32> r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) put_bits(r, i, i >= lo && i < hi ? load_bits<F32>(p, at + i) : 0u);
+  return r;
+}
+template <int F32>
+__device__ __forceinline__ void store_cols(void *p, int64_t at, bool vec, int lo, int hi,
+                                           const Row8<F32> &r) {
   if (vec) {
     store8<F32>(p, at, r);
     return;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (i >= lo && i < hi) {
-      if (F32)
-        static_cast<uint32_t *>(p)[at + i] = r.w[i >> 2][i & 3];
-      else
-        static_cast<uint16_t *>(p)[at + i] = (uint16_t)(r.w[0][i >> 1] >> (16 * (i & 1)));
-    }
-}
-
-// What the epilogue reads for 8 columns of a row, loaded ahead of its use.
-// Columns [lo, hi) of the eight are the output's; `vec`: all of them, at an
-// address for 16-byte accesses in every matrix the call has.
-template <int F32, bool GRAD>
-struct EpiIn {
-  Row8<F32> mul, other;          // other: the residual, or pre for a gradient
-
-  __device__ __forceinline__ void load(const EpiArgs &e, int64_t row, int64_t col, bool vec, int lo,
-                                       int hi) {
-    if (e.mul) mul = epi_load<F32>(e.mul, row * e.ldmul + col, vec, lo, hi);
-    if (GRAD)
-      other = epi_load<F32>(e.pre, row * e.ldpre + col, vec, lo, hi);
-    else if (e.residual)
-      other = epi_load<F32>(e.residual, row * e.ldres + col, vec, lo, hi);
-  }
-};
-
-// Columns [lo, hi) of the 8 from (row, col) on, given their sums v.
-template <int F32, bool GRAD>
-__device__ __forceinline__ void epilogue8(const EpiArgs &e, void *c, int64_t ldc, float (&v)[8],
-                                          const EpiIn<F32, GRAD> &in, const float (&bias)[8],
-                                          int64_t row, int64_t col, bool vec, int lo, int hi) {
-  float m[8], o[8];
-  if (e.mul) widen8<F32>(in.mul, m);
-  if (GRAD) {
-    widen8<F32>(in.other, o);
-    float d[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float slope;
-      const float y = act_both(o[i], e.act, slope);
-      d[i] = v[i] * y;
-      v[i] *= slope;
-      if (e.mul) v[i] *= m[i];
-    }
-    if (e.dmul) epi_store<F32>(e.dmul, row * e.lddmul + col, vec, lo, hi, d);
-  } else {
-    if (e.bias) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += bias[i];
-    }
-    if (e.pre) epi_store<F32>(e.pre, row * e.ldpre + col, vec, lo, hi, v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = act_value(v[i], e.act);
-    if (e.mul) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= m[i];
-    }
-    if (e.residual) {
-      widen8<F32>(in.other, o);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += o[i];
-    }
-  }
-  epi_store<F32>(c, row * ldc + col, vec, lo, hi, v);
-}
-
-// Bias of 8 columns (of a group's row of biases from element `at` on).
-__device__ __forceinline__ void epi_bias(const EpiArgs &e, int64_t at, int lo, int hi,
-                                         float (&bias)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    bias[i] = 0.0f;
-    if (e.bias && i >= lo && i < hi)
-      bias[i] = e.bias_f32 ? static_cast<const float *>(e.bias)[at + i]
-                           : bits_f((uint32_t) static_cast<const uint16_t *>(e.bias)[at + i] << 16);
-  }
+    if (i >= lo && i < hi) store_bits<F32>(p, at + i, r, i);
 }
 
 }  // namespace mx

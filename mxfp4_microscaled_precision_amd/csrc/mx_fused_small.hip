@@ -139,11 +139,16 @@ __global__ __launch_bounds__(64 * kWaves) void fused_small_kernel(FusedArgs g, i
   const int lo = max(0, -col), hi = min(8, g.N - col);
   const bool live = tid < kRows * 8 && row >= first && row < last && lo < hi;
   const bool vec = g.e.vec && lo == 0 && hi == 8 && (col & 7) == 0;
-  EpiIn<F32, GRAD> in;
+  Row8<F32> mul, other, c, second;
   float bias[8];
   if (live) {
-    in.load(g.e, c_row + row, col, vec, lo, hi);
-    epi_bias(g.e, (int64_t)e * g.N + col, lo, hi, bias);
+    if (g.e.mul) mul = load_cols<F32>(g.e.mul, (c_row + row) * g.e.ldmul + col, vec, lo, hi);
+    if (other_of<GRAD>(g.e))
+      other = load_cols<F32>(other_of<GRAD>(g.e), (c_row + row) * other_ld<GRAD>(g.e) + col, vec,
+                             lo, hi);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      bias[i] = g.e.bias && i >= lo && i < hi ? load_bias(g.e, (int64_t)e * g.N + col + i) : 0.0f;
   }
   __syncthreads();
   if (!live) return;
@@ -158,7 +163,13 @@ __global__ __launch_bounds__(64 * kWaves) void fused_small_kernel(FusedArgs g, i
       for (int i = 0; i < 4; ++i) v[4 * h + i] += d[i];
     }
   }
-  epilogue8<F32, GRAD>(g.e, g.c, g.ldc, v, in, bias, c_row + row, col, vec, lo, hi);
+  with_act(g.e.act, [&](auto act) {
+    epilogue8<F32, GRAD, act()>(v, bias, g.e.mul, g.e.residual, mul, other, c, second);
+  });
+  if (second_of<GRAD>(g.e))
+    store_cols<F32>(second_of<GRAD>(g.e), (c_row + row) * second_ld<GRAD>(g.e) + col, vec, lo, hi,
+                    second);
+  store_cols<F32>(g.c, (c_row + row) * g.ldc + col, vec, lo, hi, c);
 }
 
 template <int R, int F32, bool GRAD>
@@ -188,7 +199,7 @@ hipError_t launch_rows(const FusedArgs &g, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t fused_launch(const FusedArgs &g, hipStream_t stream) {
+hipError_t fused_small_launch(const FusedArgs &g, hipStream_t stream) {
   return g.M <= 16 ? launch_rows<1>(g, stream) : launch_rows<4>(g, stream);
 }
 

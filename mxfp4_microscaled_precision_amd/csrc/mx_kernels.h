@@ -131,6 +131,9 @@ struct FusedArgs {
   EpiArgs e;
 };
 
+// Few rows (or any sizes): 64 columns of 16 or 64 rows to a workgroup.
+hipError_t fused_small_launch(const FusedArgs &g, hipStream_t stream);
+// By sizes that kernel, or tiles of 256 columns.
 hipError_t fused_launch(const FusedArgs &g, hipStream_t stream);
 
 // Gathered rows in groups, quantized in both orientations, and their sums.
