@@ -97,7 +97,7 @@ __device__ __forceinline__ float act_both(float z, float &slope) {
 // Calls f with the activation as a constant: one branch where f's elements
 // would otherwise branch each (and wait for each other's exponentials).
 template <typename F>
-__device__ __forceinline__ void with_act(int act, F f) {
+__host__ __device__ __forceinline__ void with_act(int act, F f) {
   switch (act) {
     case MX_K_ACT_RELU: f(std::integral_constant<int, MX_K_ACT_RELU>()); break;
     case MX_K_ACT_SILU: f(std::integral_constant<int, MX_K_ACT_SILU>()); break;
@@ -107,58 +107,90 @@ __device__ __forceinline__ void with_act(int act, F f) {
   }
 }
 
-// The epilogue of eight elements, whose stored values of mul and of the residual
-// (of pre, for a gradient) are in `mul` and `other`: C in c, pre (dmul, for a
-// gradient) in second, as stored. Four elements at a time: enough to overlap
-// their exponentials, and little that is live besides the sums (a wave of the
-// tile kernel holds 128 of them).
-template <int F32, bool GRAD, int ACT>
-__device__ __forceinline__ void epilogue8(const float (&v)[8], const float (&bias)[8], bool has_mul,
-                                          bool has_residual, const Row8<F32> &mul,
-                                          const Row8<F32> &other, Row8<F32> &c, Row8<F32> &second) {
-  auto element = [](const Row8<F32> &r, int i) {
-    if constexpr (F32)
-      return bits_f(r.w[i >> 2][i & 3]);
-    else
-      return bits_f(i & 1 ? r.w[0][i >> 1] & 0xFFFF0000u : r.w[0][i >> 1] << 16);
-  };
-  auto put = [](Row8<F32> &r, int i, const float (&x)[4]) {      // elements i .. i + 3
+// A unit is 16 bytes of a row: 8 bf16 elements or 4 fp32 ones.
+template <int F32>
+constexpr int kUnit = F32 ? 4 : 8;
+
+template <int F32>
+__device__ __forceinline__ float unit_element(const row_u32x4 &r, int i) {
+  if constexpr (F32)
+    return bits_f(r[i]);
+  else
+    return bits_f(i & 1 ? r[i >> 1] & 0xFFFF0000u : r[i >> 1] << 16);
+}
+
+// Elements i .. i + N - 1, rounded to the unit's type.
+template <int F32, int N>
+__device__ __forceinline__ void unit_put(row_u32x4 &r, int i, const float (&x)[N]) {
 #pragma unroll
-    for (int k = 0; k < 4; k += F32 ? 1 : 2) {
-      if constexpr (F32) {
-        r.w[i >> 2][k] = f_bits(x[k]);
-      } else {
-        typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
-        typedef float f2 __attribute__((ext_vector_type(2)));
-        r.w[0][(i + k) >> 1] =
-            __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{x[k], x[k + 1]}), bf2));
-      }
+  for (int k = 0; k < N; k += F32 ? 1 : 2) {
+    if constexpr (F32) {
+      r[i + k] = f_bits(x[k]);
+    } else {
+      typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+      typedef float f2 __attribute__((ext_vector_type(2)));
+      r[(i + k) >> 1] =
+          __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{x[k], x[k + 1]}), bf2));
     }
-  };
+  }
+}
+
+// The epilogue of one unit, whose stored values of mul and of the residual (of
+// pre, for a gradient) are in `mul` and `other`: C in c, pre (dmul, for a
+// gradient) in second, as stored. Four elements at a time (two of a gradient's):
+// enough to overlap their exponentials, and little that is live besides the sums
+// (a wave of the tile kernel holds 128 of them).
+template <int F32, bool GRAD, int ACT>
+__device__ __forceinline__ void epilogue_unit(const float (&v)[kUnit<F32>],
+                                              const float (&bias)[kUnit<F32>], bool has_mul,
+                                              bool has_residual, const row_u32x4 &mul,
+                                              const row_u32x4 &other, row_u32x4 &c,
+                                              row_u32x4 &second) {
+  constexpr int n = GRAD ? 2 : 4;
 #pragma unroll
-  for (int i = 0; i < 8; i += 4) {
-    float a[4], b[4];
+  for (int i = 0; i < kUnit<F32>; i += n) {
+    float a[n], b[n];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < n; ++k) {
       if (GRAD) {
         float slope;
-        b[k] = v[i + k] * act_both<ACT>(element(other, i + k), slope);
+        b[k] = v[i + k] * act_both<ACT>(unit_element<F32>(other, i + k), slope);
         a[k] = v[i + k] * slope;
       } else {
         b[k] = v[i + k] + bias[i + k];
         a[k] = act_value<ACT>(b[k]);
       }
     }
-    put(second, i, b);
+    unit_put<F32>(second, i, b);
     if (has_mul) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) a[k] *= element(mul, i + k);
+      for (int k = 0; k < n; ++k) a[k] *= unit_element<F32>(mul, i + k);
     }
     if (!GRAD && has_residual) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) a[k] += element(other, i + k);
+      for (int k = 0; k < n; ++k) a[k] += unit_element<F32>(other, i + k);
     }
-    put(c, i, a);
+    unit_put<F32>(c, i, a);
+    if (GRAD) __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// Eight elements as one unit of bf16 or two of fp32.
+template <int F32, bool GRAD, int ACT>
+__device__ __forceinline__ void epilogue8(const float (&v)[8], const float (&bias)[8], bool has_mul,
+                                          bool has_residual, const Row8<F32> &mul,
+                                          const Row8<F32> &other, Row8<F32> &c, Row8<F32> &second) {
+  constexpr int n = kUnit<F32>;
+#pragma unroll
+  for (int h = 0; h < 8 / n; ++h) {
+    float x[n], y[n];
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      x[i] = v[n * h + i];
+      y[i] = bias[n * h + i];
+    }
+    epilogue_unit<F32, GRAD, ACT>(x, y, has_mul, has_residual, mul.w[h], other.w[h], c.w[h],
+                                  second.w[h]);
   }
 }
 
