@@ -21,6 +21,10 @@
 
 namespace mx {
 
+// Direction of an epilogue, constant where the tile kernel's registers depend on
+// it: forward, or a gradient without and with mul.
+enum { kForward = 0, kGradient = 1, kGradientMul = 2 };
+
 constexpr float kLog2e = 1.44269504f;
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -50,35 +54,43 @@ __device__ __forceinline__ float erfc_scaled(float z, float &e) {
 // 0.044715 z^3), as (1 + tanh v) / 2 is the logistic function of 2 v.
 constexpr float kGelu1 = 1.59576912f, kGelu3 = 0.0713548163f;
 
-// act(z). The limits at the infinities; NaN stays NaN. (A product with -1e30
-// in -inf's place keeps the limit 0 where the formula has -inf * 0.)
+// z, but -1e30 for what is below it (NaN stays NaN): the limit of z p at -inf is
+// then 0 where the formula has -inf * 0. One v_maximum3_f32.
+__device__ __forceinline__ float from_below(float z) {
+  return __builtin_elementwise_maximum(z, -1e30f);
+}
+
+// act(z). The limits at the infinities; NaN stays NaN.
 template <int act>
 __device__ __forceinline__ float act_value(float z) {
-  if (act == MX_K_ACT_SILU) return fmaxf(z, -1e30f) * logistic(z);
+  if (act == MX_K_ACT_SILU) return from_below(z) * logistic(z);
   if (act == MX_K_ACT_GELU_TANH)
-    return fmaxf(z, -1e30f) * logistic(z * __builtin_fmaf(kGelu3 * z, z, kGelu1));
+    return from_below(z) * logistic(z * __builtin_fmaf(kGelu3 * z, z, kGelu1));
   if (act == MX_K_ACT_NONE) return z;
   const float up = __builtin_elementwise_maximum(z, 0.0f);
   if (act == MX_K_ACT_RELU) return up;
   // exact GELU: z Phi(z) = max(z, 0) - |z| erfc(|z| / sqrt 2) / 2 (no difference
-  // of near numbers below zero)
+  // of near numbers below zero; from |z| = 64 on the second term is 0)
   float e;
   const float c = erfc_scaled(z, e);
-  return __builtin_fmaf(-0.5f * fminf(fabsf(z), 64.0f), c, up);
+  return __builtin_fmaf(-0.5f * __builtin_amdgcn_fmed3f(fabsf(z), 0.0f, 64.0f), c, up);
 }
 
-// act(z) and act'(z). Beyond +-64 the slopes are 0 and 1 in fp32, so the
-// clamp only keeps infinity * 0 away.
+// act(z) and act'(z). Beyond +-64 the slopes are 0 and 1 in fp32, so the clamp
+// only keeps infinity * 0 away (a NaN comes back through p or c).
 template <int act>
 __device__ __forceinline__ float act_both(float z, float &slope) {
-  const float zc = __builtin_amdgcn_fmed3f(z, -128.0f, 128.0f);
-  if (act == MX_K_ACT_SILU || act == MX_K_ACT_GELU_TANH) {
-    const bool tanh_form = act == MX_K_ACT_GELU_TANH;
-    const float z2 = kGelu3 * zc * zc;
-    const float p = logistic(tanh_form ? z * __builtin_fmaf(kGelu3 * z, z, kGelu1) : z);
-    const float du = tanh_form ? __builtin_fmaf(3.0f, z2, kGelu1) : 1.0f;
+  const float zc = __builtin_amdgcn_fmed3f(z, -64.0f, 64.0f);
+  if (act == MX_K_ACT_SILU) {              // slope p + z p (1 - p)
+    const float p = logistic(z);
+    slope = __builtin_fmaf(zc * p, 1.0f - p, p);
+    return from_below(z) * p;
+  }
+  if (act == MX_K_ACT_GELU_TANH) {         // slope p + z p (1 - p) u'
+    const float p = logistic(z * __builtin_fmaf(kGelu3 * z, z, kGelu1));
+    const float du = __builtin_fmaf(3.0f * kGelu3 * zc, zc, kGelu1);
     slope = __builtin_fmaf(zc * p * (1.0f - p), du, p);
-    return fmaxf(z, -1e30f) * p;
+    return from_below(z) * p;
   }
   slope = 1.0f;
   if (act == MX_K_ACT_NONE) return z;
@@ -87,11 +99,10 @@ __device__ __forceinline__ float act_both(float z, float &slope) {
     slope = z > 0.0f ? 1.0f : 0.0f;
     return up;
   }
-  float e;
+  float e;                                 // slope Phi(z) + z phi(z)
   const float c = 0.5f * erfc_scaled(z, e);
   slope = __builtin_fmaf(zc * 0.398942280f, e, z > 0.0f ? 1.0f - c : c);
-  if (z != z) slope = z;
-  return __builtin_fmaf(-fminf(fabsf(z), 64.0f), c, up);
+  return __builtin_fmaf(-fabsf(zc), c, up);
 }
 
 // Calls f with the activation as a constant: one branch where f's elements
@@ -135,17 +146,18 @@ __device__ __forceinline__ void unit_put(row_u32x4 &r, int i, const float (&x)[N
   }
 }
 
-// The epilogue of one unit, whose stored values of mul and of the residual (of
-// pre, for a gradient) are in `mul` and `other`: C in c, pre (dmul, for a
-// gradient) in second, as stored. Four elements at a time (two of a gradient's):
+// The epilogue of one unit (v: its sums, the bias added), whose stored values of
+// mul and of the residual (of pre, for a gradient) are in `mul` and `other`: C in
+// c, pre (dmul, for a gradient) in second, as stored. Four elements at a time (two of a gradient's):
 // enough to overlap their exponentials, and little that is live besides the sums
 // (a wave of the tile kernel holds 128 of them).
-template <int F32, bool GRAD, int ACT>
-__device__ __forceinline__ void epilogue_unit(const float (&v)[kUnit<F32>],
-                                              const float (&bias)[kUnit<F32>], bool has_mul,
+template <int F32, int MODE, int ACT>
+__device__ __forceinline__ void epilogue_unit(const float (&v)[kUnit<F32>], bool has_mul,
                                               bool has_residual, const row_u32x4 &mul,
                                               const row_u32x4 &other, row_u32x4 &c,
                                               row_u32x4 &second) {
+  constexpr bool GRAD = MODE != kForward;
+  if (GRAD) has_mul = MODE == kGradientMul;
   constexpr int n = GRAD ? 2 : 4;
 #pragma unroll
   for (int i = 0; i < kUnit<F32>; i += n) {
@@ -157,7 +169,7 @@ __device__ __forceinline__ void epilogue_unit(const float (&v)[kUnit<F32>],
         b[k] = v[i + k] * act_both<ACT>(unit_element<F32>(other, i + k), slope);
         a[k] = v[i + k] * slope;
       } else {
-        b[k] = v[i + k] + bias[i + k];
+        b[k] = v[i + k];
         a[k] = act_value<ACT>(b[k]);
       }
     }
@@ -183,14 +195,15 @@ __device__ __forceinline__ void epilogue8(const float (&v)[8], const float (&bia
   constexpr int n = kUnit<F32>;
 #pragma unroll
   for (int h = 0; h < 8 / n; ++h) {
-    float x[n], y[n];
+    float x[n];
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
-      x[i] = v[n * h + i];
-      y[i] = bias[n * h + i];
-    }
-    epilogue_unit<F32, GRAD, ACT>(x, y, has_mul, has_residual, mul.w[h], other.w[h], c.w[h],
-                                  second.w[h]);
+    for (int i = 0; i < n; ++i) x[i] = GRAD ? v[n * h + i] : v[n * h + i] + bias[n * h + i];
+    if (GRAD && !has_mul)
+      epilogue_unit<F32, kGradient, ACT>(x, false, false, mul.w[h], other.w[h], c.w[h],
+                                         second.w[h]);
+    else
+      epilogue_unit<F32, GRAD ? kGradientMul : kForward, ACT>(
+          x, has_mul, has_residual, mul.w[h], other.w[h], c.w[h], second.w[h]);
   }
 }
 

@@ -123,10 +123,7 @@ __device__ __forceinline__ Plan make_plan(const FusedArgs &g, const int *units) 
   p.row_tiles = g.kind == MX_K_WGRAD ? g.groups * tm
                 : g.ends             ? uniform_word(units + g.groups - 1)
                                      : tm;
-  // a group's columns may begin at any row of B
-  p.col_tiles = (g.N + kBN - 1) / kBN;
-  if (g.kind == MX_K_FPROP && g.groups > 1 && (g.N & 63) != 0)
-    p.col_tiles = (g.N + 63 + kBN - 1) / kBN;
+  p.col_tiles = g.col_tiles;
   p.total = p.row_tiles * p.col_tiles;
   const int rem = p.total % grid;
   const bool cut = rem != 0 && 2 * rem <= grid;
@@ -151,11 +148,12 @@ __device__ __forceinline__ Tile tile_at(const FusedArgs &g, const Plan &p, const
     half = bid & 1;
     if (p.whole == p.total) half = -1;      // (not reached: mine counts no such tile)
   }
-  const int per_group = kGroupM * p.col_tiles;
-  const int grp = id / per_group, first_row = grp * kGroupM;
+  static_assert(kGroupM == 4, "divisions below");
+  const int grp = g.by_col_tiles(id >> 2), first_row = grp * kGroupM;
   const int gm = min(kGroupM, p.row_tiles - first_row);
-  const int r = id - grp * per_group;
-  const int rt = first_row + r % gm, ct = r / gm;
+  const int r = id - grp * kGroupM * p.col_tiles;
+  const int ct = gm == 4 ? r >> 2 : gm == 3 ? r / 3 : gm == 2 ? r >> 1 : r;
+  const int rt = first_row + r - ct * gm;
 
   Tile t;
   t.e = 0;
@@ -166,7 +164,7 @@ __device__ __forceinline__ Tile tile_at(const FusedArgs &g, const Plan &p, const
   t.rb = t.col0 = ct * kBN;
   if (g.kind == MX_K_WGRAD) {
     const int tm = (g.M + kBM - 1) / kBM;
-    t.e = rt / tm;
+    t.e = g.by_row_tiles(rt);
     t.ra = (rt - t.e * tm) * kBM;
     t.ka = t.kb = t.e ? uniform_word(units + t.e - 1) : 0;
     t.nk = uniform_word(units + t.e) - t.ka;
@@ -303,10 +301,11 @@ struct Rows {
 // mul and the residual of a unit are asked for one unit ahead at first and up to
 // four once the accumulators of finished units leave registers for them; each
 // request goes out before its unit's stores, so that no load waits for a store.
-template <int F32, bool GRAD, int ACT>
+template <int F32, int MODE, int ACT>
 __device__ __forceinline__ void finish_rows(const FusedArgs &g, const Tile &t,
                                             const v4f (&acc)[kRows][4], const float *columns,
                                             int64_t c_row, int row0, int col0, int live, int lane) {
+  constexpr bool GRAD = MODE != kForward;
   constexpr int kSize = F32 ? 4 : 2, n = kUnit<F32>;
   constexpr int kPerStrip = F32 ? 4 : 2;           // units of a lane in a strip
   constexpr int kUnits = kPerStrip * kRows, kSlots = 5;
@@ -314,19 +313,17 @@ __device__ __forceinline__ void finish_rows(const FusedArgs &g, const Tile &t,
   const Rows po(other_of<GRAD>(g.e), other_ld<GRAD>(g.e), c_row + row0, col0, kSize);
   const Rows p2(second_of<GRAD>(g.e), second_ld<GRAD>(g.e), c_row + row0, col0, kSize);
   const Rows pc(g.c, g.ldc, c_row + row0, col0, kSize);
-  // first column of the lane's unit 0 (of a pair), and its byte in a strip of
-  // matrix m, unit u; rows that are not the tile's are outside. Made anew each
-  // time: kept, they would cost registers that the accumulators need.
-  auto first = [&](int l) {
-    const int lg = l >> 4;
-    return F32 ? 4 * lg : 16 * (lg & 1) + 8 * (lg >> 1);
-  };
-  auto at = [&](const Rows &m, int u) {
-    int l = lane;
-    asm volatile("" : "+v"(l));
-    const int row = row0 + 16 * (u / kPerStrip) + (l & 15);
-    const uint32_t b = __umul24(l & 15, m.pitch) + first(l) * kSize + (u % kPerStrip) * 64;
-    return row >= t.first && row < t.last ? b : kOutside;
+  // Byte of this lane in a strip of matrix m: one multiply-add, made anew at every
+  // use (the compiler would hold one register per matrix, and spill). Rows that
+  // are not the tile's are outside.
+  const int lg = lane >> 4;
+  const uint32_t lr = lane & 15;
+  const uint32_t c0 = (F32 ? 4 * lg : 16 * (lg & 1) + 8 * (lg >> 1)) * kSize;
+  const int before = t.first - row0, count = t.last - t.first;
+  auto at = [&](const Rows &m, int i) {
+    uint32_t b;
+    asm volatile("v_mad_u32_u24 %0, %1, %2, %3" : "=v"(b) : "v"(lr), "s"(m.pitch), "v"(c0));
+    return lr + (uint32_t)(16 * i - before) < (uint32_t)count ? b : kOutside;
   };
   // the last unit asked for when unit u is done
   constexpr int kWait = (GRAD ? 4 : 2) * kPerStrip / 2, kSlow = F32 ? 4 : GRAD ? 3 : 2;
@@ -337,16 +334,16 @@ __device__ __forceinline__ void finish_rows(const FusedArgs &g, const Tile &t,
   row_u32x4 mul[kSlots], other[kSlots];
   auto load = [&](auto unit) {
     constexpr int u = unit();
-    if (u >= kUnits || u / kPerStrip >= live) return;
-    const uint32_t row = 16 * (u / kPerStrip);
-    if (pm.any) mul[u % kSlots] = pm.load(at(pm, u), row);
-    if (po.any) other[u % kSlots] = po.load(at(po, u), row);
+    constexpr int i = u / kPerStrip, byte = (u % kPerStrip) * 64;
+    if (u >= kUnits || i >= live) return;
+    if (GRAD ? MODE == kGradientMul : pm.any) mul[u % kSlots] = pm.load(at(pm, i) + byte, 16 * i);
+    if (GRAD || po.any) other[u % kSlots] = po.load(at(po, i) + byte, 16 * i);
   };
   load(std::integral_constant<int, 0>());
   for_each_int<kUnits>([&](auto unit) {
     constexpr int u = unit(), i = u / kPerStrip, q = u % kPerStrip;
     if (i < live) {
-      float v[n], bias[n];
+      float v[n];
       if constexpr (F32) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] = acc[i][q][k];
@@ -359,27 +356,26 @@ __device__ __forceinline__ void finish_rows(const FusedArgs &g, const Tile &t,
           v[k + 4] = bits_f(r[1]);
         }
       }
-#pragma unroll
-      for (int k = 0; k < n; ++k) bias[k] = 0.0f;
       if (!GRAD && g.e.bias) {
-        int l = lane;
-        asm volatile("" : "+v"(l));
 #pragma unroll
         for (int k = 0; k < n; k += 4) {
-          const v4f b = *reinterpret_cast<const v4f *>(columns + first(l) + q * (F32 ? 16 : 32) + k);
+          const v4f b = *reinterpret_cast<const v4f *>(columns + c0 / kSize + q * (64 / kSize) + k);
 #pragma unroll
-          for (int h = 0; h < 4; ++h) bias[k + h] = b[h];
+          for (int h = 0; h < 4; ++h) v[k + h] += b[h];
         }
       }
       row_u32x4 c, second;
-      epilogue_unit<F32, GRAD, ACT>(v, bias, pm.any, !GRAD && po.any, mul[u % kSlots],
-                                    other[u % kSlots], c, second);
+      epilogue_unit<F32, MODE, ACT>(v, pm.any, po.any, mul[u % kSlots], other[u % kSlots], c,
+                                    second);
       __builtin_amdgcn_sched_barrier(0);
       constexpr int done = u == 0 ? 0 : requested(u - 1), more = requested(u) - done;
       load(std::integral_constant<int, done + 1>());
       if constexpr (more > 1) load(std::integral_constant<int, done + 2>());
-      if (p2.any) p2.store(second, at(p2, u), 16 * i);
-      pc.store(c, at(pc, u), 16 * i);
+      constexpr int byte = q * 64;
+      // (a store into no matrix does nothing; a branch around it would move what
+      // it stores behind it, and hold every element's exponential up to there)
+      if (GRAD ? MODE == kGradientMul : p2.any) p2.store(second, at(p2, i) + byte, 16 * i);
+      pc.store(c, at(pc, i) + byte, 16 * i);
       __builtin_amdgcn_sched_barrier(0);
     }
   });
@@ -387,11 +383,12 @@ __device__ __forceinline__ void finish_rows(const FusedArgs &g, const Tile &t,
 
 // The same element by element: lane l has column l of the step's eight rows, so
 // that 64 lanes still access 64 adjacent columns.
-template <int F32, bool GRAD, int ACT>
+template <int F32, int MODE, int ACT>
 __device__ __forceinline__ void finish_columns(const FusedArgs &g, const Tile &t,
                                                const v4f (&acc)[kRows][4], uint8_t *slab,
                                                const float *columns, int64_t c_row, int row0,
                                                int col0, int live, int lane) {
+  constexpr bool GRAD = MODE != kForward;
 #pragma clang loop unroll(disable)
   for (int s = 0; s < 2 * live; ++s) {
     int l = lane;
@@ -434,7 +431,7 @@ __device__ __forceinline__ void finish_columns(const FusedArgs &g, const Tile &t
 
 // The wave's part of a finished tile: `live` strips of 16 rows x 64 columns. The
 // bias of its columns waits in LDS (`columns`): eight registers less.
-template <int F32, bool GRAD, int ACT>
+template <int F32, int MODE, int ACT>
 __device__ __forceinline__ void finish(const Tile &t,
                                        const v4f (&acc)[kRows][4], uint8_t *slab, float *columns,
                                        int row0, int col0, int live, int lane) {
@@ -448,9 +445,9 @@ __device__ __forceinline__ void finish(const Tile &t,
   wave_sync();
   const bool vec = g.e.vec && (col0 & 7) == 0 && col0 >= 0 && col0 + 64 <= g.N;
   if (vec)
-    finish_rows<F32, GRAD, ACT>(g, t, acc, columns, c_row, row0, col0, live, lane);
+    finish_rows<F32, MODE, ACT>(g, t, acc, columns, c_row, row0, col0, live, lane);
   else
-    finish_columns<F32, GRAD, ACT>(g, t, acc, slab, columns, c_row, row0, col0, live, lane);
+    finish_columns<F32, MODE, ACT>(g, t, acc, slab, columns, c_row, row0, col0, live, lane);
 }
 
 // One tile's stages, from stage G of the ring on. SHIFTED waves run most of a
@@ -487,7 +484,7 @@ __device__ __forceinline__ void stages(v4f (&acc)[kRows][4], const uint8_t *smem
 }
 
 // A multiplying wave's tiles.
-template <int F32, bool GRAD, int ACT, bool SHIFTED>
+template <int F32, int MODE, int ACT, bool SHIFTED>
 __device__ __forceinline__ void consume(const Plan &p, uint8_t *smem,
                                         const int *ends, const int *units, int lane, int wn) {
   constexpr int wm = SHIFTED ? 1 : 0;
@@ -522,7 +519,7 @@ __device__ __forceinline__ void consume(const Plan &p, uint8_t *smem,
     // the tile is looked up again: what it says would hold registers through
     // the stages
     const Tile t = tile_at(read_again(), p, ends, units, k);
-    finish<F32, GRAD, ACT>(t, acc, slab, columns, t.ra + wm * part, t.col0 + wn * 64, live, lane);
+    finish<F32, MODE, ACT>(t, acc, slab, columns, t.ra + wm * part, t.col0 + wn * 64, live, lane);
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
 #pragma unroll
@@ -531,7 +528,7 @@ __device__ __forceinline__ void consume(const Plan &p, uint8_t *smem,
   if (!SHIFTED) __syncthreads();                           // the shifted waves' last barrier
 }
 
-template <int F32, bool GRAD, int ACT>
+template <int F32, int MODE, int ACT>
 __global__ __launch_bounds__(kThreads, 1) void fused_tile_kernel(FusedArgs g) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[kTable];
   __shared__ int ends[kTileGroups], units[kTileGroups];
@@ -544,9 +541,9 @@ __global__ __launch_bounds__(kThreads, 1) void fused_tile_kernel(FusedArgs g) {
   const Plan plan = make_plan(g, units);
   if (wave < kConsumers) {
     if (wave >> 2)
-      consume<F32, GRAD, ACT, true>(plan, smem, ends, units, lane, wave & 3);
+      consume<F32, MODE, ACT, true>(plan, smem, ends, units, lane, wave & 3);
     else
-      consume<F32, GRAD, ACT, false>(plan, smem, ends, units, lane, wave & 3);
+      consume<F32, MODE, ACT, false>(plan, smem, ends, units, lane, wave & 3);
     return;
   }
 
@@ -627,11 +624,11 @@ __global__ __launch_bounds__(kThreads, 1) void fused_tile_kernel(FusedArgs g) {
 }
 
 // The kernel of one output type and direction, for the call's activation.
-template <int F32, bool GRAD>
+template <int F32, int MODE>
 hipError_t launch_tiles(const FusedArgs &g, dim3 grid, hipStream_t stream) {
   hipError_t e = hipErrorInvalidValue;
   with_act(g.e.act, [&](auto act) {
-    e = launch(fused_tile_kernel<F32, GRAD, act()>, grid, dim3(kThreads), 0, stream, g);
+    e = launch(fused_tile_kernel<F32, MODE, act()>, grid, dim3(kThreads), 0, stream, g);
   });
   return e;
 }
@@ -643,5 +640,7 @@ hipError_t launch_tiles_bf16(const FusedArgs &g, dim3 grid, hipStream_t stream);
 hipError_t launch_tiles_f32(const FusedArgs &g, dim3 grid, hipStream_t stream);
 hipError_t launch_tiles_bf16_grad(const FusedArgs &g, dim3 grid, hipStream_t stream);
 hipError_t launch_tiles_f32_grad(const FusedArgs &g, dim3 grid, hipStream_t stream);
+hipError_t launch_tiles_bf16_grad_mul(const FusedArgs &g, dim3 grid, hipStream_t stream);
+hipError_t launch_tiles_f32_grad_mul(const FusedArgs &g, dim3 grid, hipStream_t stream);
 
 }  // namespace mx

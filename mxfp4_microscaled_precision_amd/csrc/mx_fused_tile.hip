@@ -5,20 +5,29 @@
 namespace mx {
 
 hipError_t launch_tiles_bf16(const FusedArgs &g, dim3 grid, hipStream_t stream) {
-  return tile::launch_tiles<0, false>(g, grid, stream);
+  return tile::launch_tiles<0, kForward>(g, grid, stream);
 }
 
-static hipError_t fused_tile_launch(const FusedArgs &g, hipStream_t stream) {
+static hipError_t fused_tile_launch(FusedArgs g, hipStream_t stream) {
   // at most this many tiles: a ragged group has up to two more than its rows'
   int64_t rt = ((int64_t)g.M + tile::kBM - 1) / tile::kBM;
   if (g.kind == MX_K_WGRAD)
     rt *= g.groups;
   else if (g.ends)
     rt = g.rows / tile::kBM + 2 * (int64_t)std::min(g.groups, g.rows);
-  const int64_t tiles = rt * ((g.N + 63 + tile::kBN - 1) / tile::kBN);
+  // a group's columns may begin at any row of B
+  const int64_t cols =
+      (int64_t)g.N + (g.kind == MX_K_FPROP && g.groups > 1 && g.N % 64 != 0 ? 63 : 0);
+  g.col_tiles = (int)((cols + tile::kBN - 1) / tile::kBN);
+  g.by_col_tiles = DivideBy((uint32_t)g.col_tiles);
+  g.by_row_tiles = DivideBy((uint32_t)((g.M + tile::kBM - 1) / tile::kBM));
+  const int64_t tiles = rt * g.col_tiles;
   if (tiles == 0) return hipSuccess;
   if (tiles > INT32_MAX / 2 || g.groups > tile::kTileGroups) return hipErrorInvalidValue;
   const dim3 grid((unsigned)std::min<int64_t>(2 * tiles, cu_count()));
+  if (g.grad && g.e.mul)
+    return g.out_bf16 ? launch_tiles_bf16_grad_mul(g, grid, stream)
+                      : launch_tiles_f32_grad_mul(g, grid, stream);
   if (g.grad)
     return g.out_bf16 ? launch_tiles_bf16_grad(g, grid, stream)
                       : launch_tiles_f32_grad(g, grid, stream);

@@ -4,7 +4,7 @@
 namespace mx {
 
 hipError_t launch_tiles_f32_grad(const FusedArgs &g, dim3 grid, hipStream_t stream) {
-  return tile::launch_tiles<1, true>(g, grid, stream);
+  return tile::launch_tiles<1, kGradient>(g, grid, stream);
 }
 
 }  // namespace mx

@@ -111,6 +111,21 @@ struct EpiArgs {
 
 enum { MX_K_FPROP = 0, MX_K_DGRAD = 1, MX_K_WGRAD = 2 };
 
+// n / d for 0 <= n < 2^31 by a multiplication: with 2^(l-1) < d <= 2^l and m =
+// ceil(2^(31+l) / d) < 2^32, floor(n m / 2^(31+l)) is exact (the excess n (m d -
+// 2^(31+l)) / (d 2^(31+l)) is below 1 / d).
+struct DivideBy {
+  uint32_t m = 0, l = 0;           // m == 0: by 1
+  DivideBy() = default;
+  explicit DivideBy(uint32_t d) {
+    while ((1u << l) < d) ++l;
+    if (l > 0) m = (uint32_t)((((uint64_t)1 << (31 + l)) + d - 1) / d);
+  }
+  __host__ __device__ int operator()(int n) const {
+    return m == 0 ? n : (int)(((uint64_t)(uint32_t)n * m) >> (31 + l));
+  }
+};
+
 // A product with an epilogue, of one group (dense) or of one per expert. The
 // operands are packed; C's rows are A's (fprop, dgrad) or the groups' matrices
 // one after another (wgrad).
@@ -129,6 +144,10 @@ struct FusedArgs {
   int a_panels, b_panels;          // 256-row panels of each operand
   int a_slices, b_slices;          // 128-deep slices of each operand
   EpiArgs e;
+  // set by the launcher of the tile kernel: its column tiles, and divisions by
+  // them and by the row tiles of one of wgrad's matrices
+  int col_tiles;
+  DivideBy by_col_tiles, by_row_tiles;
 };
 
 // Few rows (or any sizes): 64 columns of 16 or 64 rows to a workgroup.
