@@ -146,9 +146,33 @@ __device__ __forceinline__ void unit_put(row_u32x4 &r, int i, const float (&x)[N
   }
 }
 
-// The epilogue of one unit (v: its sums, the bias added), whose stored values of
-// mul and of the residual (of pre, for a gradient) are in `mul` and `other`: C in
-// c, pre (dmul, for a gradient) in second, as stored. Four elements at a time (two of a gradient's):
+// The epilogue of N elements: v their sums (the bias added), m(k) their mul, o(k)
+// their residual (pre, for a gradient); a becomes C, b pre (dmul, for a gradient).
+template <int MODE, int ACT, int N, typename M, typename O>
+__device__ __forceinline__ void epilogue_of(const float (&v)[N], M m, O o, bool has_mul,
+                                            bool has_residual, float (&a)[N], float (&b)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    if (MODE != kForward) {
+      float slope;
+      b[k] = v[k] * act_both<ACT>(o(k), slope);
+      a[k] = v[k] * slope;
+    } else {
+      b[k] = v[k];
+      a[k] = act_value<ACT>(v[k]);
+    }
+  }
+  if (MODE == kGradientMul || (MODE == kForward && has_mul)) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) a[k] *= m(k);
+  }
+  if (MODE == kForward && has_residual) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) a[k] += o(k);
+  }
+}
+
+// The same of one unit, as stored. Four elements at a time (two of a gradient's):
 // enough to overlap their exponentials, and little that is live besides the sums
 // (a wave of the tile kernel holds 128 of them).
 template <int F32, int MODE, int ACT>
@@ -156,34 +180,18 @@ __device__ __forceinline__ void epilogue_unit(const float (&v)[kUnit<F32>], bool
                                               bool has_residual, const row_u32x4 &mul,
                                               const row_u32x4 &other, row_u32x4 &c,
                                               row_u32x4 &second) {
-  constexpr bool GRAD = MODE != kForward;
-  if (GRAD) has_mul = MODE == kGradientMul;
-  constexpr int n = GRAD ? 2 : 4;
+  constexpr int n = MODE == kForward ? 4 : 2;
 #pragma unroll
   for (int i = 0; i < kUnit<F32>; i += n) {
-    float a[n], b[n];
+    float x[n], a[n], b[n];
 #pragma unroll
-    for (int k = 0; k < n; ++k) {
-      if (GRAD) {
-        float slope;
-        b[k] = v[i + k] * act_both<ACT>(unit_element<F32>(other, i + k), slope);
-        a[k] = v[i + k] * slope;
-      } else {
-        b[k] = v[i + k];
-        a[k] = act_value<ACT>(b[k]);
-      }
-    }
+    for (int k = 0; k < n; ++k) x[k] = v[i + k];
+    epilogue_of<MODE, ACT>(
+        x, [&](int k) { return unit_element<F32>(mul, i + k); },
+        [&](int k) { return unit_element<F32>(other, i + k); }, has_mul, has_residual, a, b);
     unit_put<F32>(second, i, b);
-    if (has_mul) {
-#pragma unroll
-      for (int k = 0; k < n; ++k) a[k] *= unit_element<F32>(mul, i + k);
-    }
-    if (!GRAD && has_residual) {
-#pragma unroll
-      for (int k = 0; k < n; ++k) a[k] += unit_element<F32>(other, i + k);
-    }
     unit_put<F32>(c, i, a);
-    if (GRAD) __builtin_amdgcn_sched_barrier(0);
+    if (MODE != kForward) __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -243,6 +251,20 @@ __device__ __forceinline__ void store_bits(void *p, int64_t at, const Row8<F32> 
     static_cast<uint32_t *>(p)[at] = r.w[i >> 2][i & 3];
   else
     static_cast<uint16_t *>(p)[at] = (uint16_t)(r.w[0][i >> 1] >> (16 * (i & 1)));
+}
+
+// One element, widened, and back.
+template <int F32>
+__device__ __forceinline__ float load_one(const void *p, int64_t at) {
+  const uint32_t b = load_bits<F32>(p, at);
+  return bits_f(F32 ? b : b << 16);
+}
+template <int F32>
+__device__ __forceinline__ void store_one(void *p, int64_t at, float v) {
+  if constexpr (F32)
+    static_cast<float *>(p)[at] = v;
+  else
+    static_cast<__bf16 *>(p)[at] = (__bf16)v;
 }
 
 // Bias of one column (element `at` of all groups' biases).

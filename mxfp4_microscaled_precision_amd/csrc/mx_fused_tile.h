@@ -195,33 +195,52 @@ __device__ __forceinline__ Tile tile_at(const FusedArgs &g, const Plan &p, const
   return t;
 }
 
-// Strip I of a wave's stage: read the A fragment two strips on (in strip S - 1
-// every one still unread), then strip I's 4 MFMAs; strips from `live` on are
-// left out. See consume_row in mx_gemm.hip.
-template <int I, int S, bool CHECK>
+// The 4 MFMAs of strip I.
+template <int I>
+__device__ __forceinline__ void multiply_strip(v4f (&acc)[kRows][4], const uint4 (&bf)[4],
+                                               const uint4 &af, uint32_t sb, uint2 sa) {
+  const uint32_t sai = I < 4 ? sa.x : sa.y;
+  acc[I][0] = mfma_fp4<0, I & 3>(bf[0], af, acc[I][0], sb, sai);
+  acc[I][1] = mfma_fp4<1, I & 3>(bf[1], af, acc[I][1], sb, sai);
+  acc[I][2] = mfma_fp4<2, I & 3>(bf[2], af, acc[I][2], sb, sai);
+  acc[I][3] = mfma_fp4<3, I & 3>(bf[3], af, acc[I][3], sb, sai);
+}
+
+// Strip I of the LIVE that a wave's stage has: read the A fragment two strips on
+// (in strip S - 1 every one still unread), then multiply. See consume_row in
+// mx_gemm.hip.
+template <int I, int S, int LIVE>
 __device__ __forceinline__ void strip(v4f (&acc)[kRows][4], const uint4 (&bf)[4],
-                                      uint4 (&af)[kRows], const uint8_t *a_base, uint32_t sb,
-                                      uint2 sa, int live) {
+                                      uint4 (&af)[LIVE], const uint8_t *a_base, uint32_t sb,
+                                      uint2 sa) {
   if (I < S) {
 #pragma unroll
-    for (int j = I + 2; j < (I == S - 1 ? kRows : I + 3); ++j)
-      if (j < kRows) af[j] = *reinterpret_cast<const uint4 *>(a_base + j * 1024);
+    for (int j = I + 2; j < (I == S - 1 ? LIVE : I + 3); ++j)
+      if (j < LIVE) af[j < LIVE ? j : 0] = *reinterpret_cast<const uint4 *>(a_base + j * 1024);
   }
-  if (!CHECK || I < live) {
-    const uint32_t sai = I < 4 ? sa.x : sa.y;
-    acc[I][0] = mfma_fp4<0, I & 3>(bf[0], af[I], acc[I][0], sb, sai);
-    acc[I][1] = mfma_fp4<1, I & 3>(bf[1], af[I], acc[I][1], sb, sai);
-    acc[I][2] = mfma_fp4<2, I & 3>(bf[2], af[I], acc[I][2], sb, sai);
-    acc[I][3] = mfma_fp4<3, I & 3>(bf[3], af[I], acc[I][3], sb, sai);
-  }
+  multiply_strip<I>(acc, bf, af[I], sb, sa);
   __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int LO, int S, bool CHECK, int... I>
+template <int LO, int S, int LIVE, int... I>
 __device__ __forceinline__ void strips(std::integer_sequence<int, I...>, v4f (&acc)[kRows][4],
-                                       const uint4 (&bf)[4], uint4 (&af)[kRows],
-                                       const uint8_t *a_base, uint32_t sb, uint2 sa, int live) {
-  (strip<LO + I, S, CHECK>(acc, bf, af, a_base, sb, sa, live), ...);
+                                       const uint4 (&bf)[4], uint4 (&af)[LIVE],
+                                       const uint8_t *a_base, uint32_t sb, uint2 sa) {
+  (strip<LO + I, S, LIVE>(acc, bf, af, a_base, sb, sa), ...);
+}
+
+// Strips 0 .. live - 1 of a stage, any number: each read when it is multiplied.
+template <int... I>
+__device__ __forceinline__ void some_strips(std::integer_sequence<int, I...>, v4f (&acc)[kRows][4],
+                                            const uint4 (&bf)[4], const uint8_t *a_base,
+                                            uint32_t sb, uint2 sa, int live) {
+  auto one = [&](auto i) {
+    if (i() < live) {
+      const uint4 af = *reinterpret_cast<const uint4 *>(a_base + i() * 1024);
+      multiply_strip<i()>(acc, bf, af, sb, sa);
+    }
+  };
+  (one(std::integral_constant<int, I>()), ...);
 }
 
 // Eight rows (half s of strip s / 2) of the wave's sums into its 2 KB of LDS:
@@ -279,12 +298,14 @@ struct Rows {
                  : nullptr,
             0, base ? kOutside : 0, 0x00020000)),
         pitch((uint32_t)(ld * esize)), any(base != nullptr) {}
-  __device__ __forceinline__ row_u32x4 load(uint32_t at, uint32_t row) const {
-    return __builtin_bit_cast(row_u32x4,
-                              __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, row * pitch, 0));
+  // `byte` bytes past the lane's offset in row `row` (both uniform)
+  __device__ __forceinline__ row_u32x4 load(uint32_t at, uint32_t row, uint32_t byte) const {
+    return __builtin_bit_cast(
+        row_u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, row * pitch + byte, 0));
   }
-  __device__ __forceinline__ void store(row_u32x4 v, uint32_t at, uint32_t row) const {
-    __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, at, row * pitch, 0);
+  __device__ __forceinline__ void store(row_u32x4 v, uint32_t at, uint32_t row,
+                                        uint32_t byte) const {
+    __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, at, row * pitch + byte, 0);
   }
 };
 
@@ -326,7 +347,7 @@ __device__ __forceinline__ void finish_rows(const FusedArgs &g, const Tile &t,
     return lr + (uint32_t)(16 * i - before) < (uint32_t)count ? b : kOutside;
   };
   // the last unit asked for when unit u is done
-  constexpr int kWait = (GRAD ? 4 : 2) * kPerStrip / 2, kSlow = F32 ? 4 : GRAD ? 3 : 2;
+  constexpr int kWait = GRAD ? 4 * kPerStrip / 2 : kPerStrip, kSlow = F32 ? 4 : GRAD ? 3 : 2;
   constexpr auto requested = [](int u) {
     const int more = u < kWait ? 0 : (u - kWait) / kSlow;
     return u + 1 + (more < 3 ? more : 3);
@@ -336,8 +357,8 @@ __device__ __forceinline__ void finish_rows(const FusedArgs &g, const Tile &t,
     constexpr int u = unit();
     constexpr int i = u / kPerStrip, byte = (u % kPerStrip) * 64;
     if (u >= kUnits || i >= live) return;
-    if (GRAD ? MODE == kGradientMul : pm.any) mul[u % kSlots] = pm.load(at(pm, i) + byte, 16 * i);
-    if (GRAD || po.any) other[u % kSlots] = po.load(at(po, i) + byte, 16 * i);
+    if (GRAD ? MODE == kGradientMul : pm.any) mul[u % kSlots] = pm.load(at(pm, i), 16 * i, byte);
+    if (GRAD || po.any) other[u % kSlots] = po.load(at(po, i), 16 * i, byte);
   };
   load(std::integral_constant<int, 0>());
   for_each_int<kUnits>([&](auto unit) {
@@ -374,15 +395,16 @@ __device__ __forceinline__ void finish_rows(const FusedArgs &g, const Tile &t,
       constexpr int byte = q * 64;
       // (a store into no matrix does nothing; a branch around it would move what
       // it stores behind it, and hold every element's exponential up to there)
-      if (GRAD ? MODE == kGradientMul : p2.any) p2.store(second, at(p2, i) + byte, 16 * i);
-      pc.store(c, at(pc, i) + byte, 16 * i);
+      if (GRAD ? MODE == kGradientMul : p2.any) p2.store(second, at(p2, i), 16 * i, byte);
+      pc.store(c, at(pc, i), 16 * i, byte);
       __builtin_amdgcn_sched_barrier(0);
     }
   });
 }
 
-// The same element by element: lane l has column l of the step's eight rows, so
-// that 64 lanes still access 64 adjacent columns.
+// The same element by element, for matrices that do not take 16-byte accesses:
+// the sums go through LDS, eight rows at a time, and lane l has column l of four
+// rows at once, so that 64 lanes still access 64 adjacent columns.
 template <int F32, int MODE, int ACT>
 __device__ __forceinline__ void finish_columns(const FusedArgs &g, const Tile &t,
                                                const v4f (&acc)[kRows][4], uint8_t *slab,
@@ -390,41 +412,38 @@ __device__ __forceinline__ void finish_columns(const FusedArgs &g, const Tile &t
                                                int col0, int live, int lane) {
   constexpr bool GRAD = MODE != kForward;
 #pragma clang loop unroll(disable)
-  for (int s = 0; s < 2 * live; ++s) {
+  for (int s = 0; s < 4 * live; ++s) {             // four rows, half s % 2 of eight
     int l = lane;
     asm volatile("" : "+v"(l));
-    const int col = col0 + l, r0 = row0 + 8 * s;
+    const int col = col0 + l, r0 = row0 + 4 * s;
     const bool in = col >= 0 && col < g.N;
+    if (!(s & 1)) {
+      wave_sync();
+      stage_rows(acc, slab, s >> 1, l);
+      wave_sync();
+    }
     const void *const from = other_of<GRAD>(g.e);
-    Row8<F32> mul, other, c, second;
+    float v[4], m[4], o[4], a[4], b[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t row = c_row + r0 + i;
-      const bool live_row = in && r0 + i >= t.first && r0 + i < t.last;
-      if (g.e.mul)
-        put_bits(mul, i, live_row ? load_bits<F32>(g.e.mul, row * g.e.ldmul + col) : 0u);
-      if (from)
-        put_bits(other, i, live_row ? load_bits<F32>(from, row * other_ld<GRAD>(g.e) + col) : 0u);
-    }
-    stage_rows(acc, slab, s, l);
-    wave_sync();
-    float v[8], bias[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = *reinterpret_cast<const float *>(slab + i * 256 + (((l >> 2) ^ (2 * i)) << 4) +
+    for (int i = 0; i < 4; ++i) {
+      const int row = r0 + i, at = 4 * (s & 1) + i;
+      const bool mine = in && row >= t.first && row < t.last;
+      m[i] = o[i] = 0.0f;
+      if (mine && g.e.mul) m[i] = load_one<F32>(g.e.mul, (c_row + row) * g.e.ldmul + col);
+      if (mine && from) o[i] = load_one<F32>(from, (c_row + row) * other_ld<GRAD>(g.e) + col);
+      v[i] = *reinterpret_cast<const float *>(slab + at * 256 + (((l >> 2) ^ (2 * at)) << 4) +
                                               (l & 3) * 4);
-      bias[i] = columns[l];
+      if (!GRAD && g.e.bias) v[i] += columns[l];
     }
-    wave_sync();
-    epilogue8<F32, GRAD, ACT>(v, bias, g.e.mul, g.e.residual, mul, other, c, second);
+    epilogue_of<MODE, ACT>(
+        v, [&](int k) { return m[k]; }, [&](int k) { return o[k]; }, g.e.mul, g.e.residual, a, b);
     void *const to2 = second_of<GRAD>(g.e);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t row = c_row + r0 + i;
-      if (in && r0 + i >= t.first && r0 + i < t.last) {
-        if (to2) store_bits<F32>(to2, row * second_ld<GRAD>(g.e) + col, second, i);
-        store_bits<F32>(g.c, row * g.ldc + col, c, i);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int row = r0 + i;
+      if (!in || row < t.first || row >= t.last) continue;
+      if (to2) store_one<F32>(to2, (c_row + row) * second_ld<GRAD>(g.e) + col, b[i]);
+      store_one<F32>(g.c, (c_row + row) * g.ldc + col, a[i]);
     }
   }
 }
@@ -450,44 +469,55 @@ __device__ __forceinline__ void finish(const Tile &t,
     finish_columns<F32, MODE, ACT>(g, t, acc, slab, columns, c_row, row0, col0, live, lane);
 }
 
-// One tile's stages, from stage G of the ring on. SHIFTED waves run most of a
-// stage behind (see consumer_loop in mx_gemm.hip). CHECK: only `live` strips.
-template <bool SHIFTED, bool CHECK>
+// One tile's stages, from stage G of the ring on, of LIVE strips (0: of `live`).
+// SHIFTED waves run most of a stage behind, and take the barrier where they have
+// read all of it (see consumer_loop in mx_gemm.hip).
+template <bool SHIFTED, int LIVE>
 __device__ __forceinline__ void stages(v4f (&acc)[kRows][4], const uint8_t *smem, int G, int nk,
                                        uint32_t a_off, uint32_t b_off, uint32_t sa_off,
                                        uint32_t sb_off, int live) {
-  constexpr int kSplit = 6;
+  constexpr int kSplit = LIVE == kRows ? 6 : 3;
   for (const int end = G + nk; G < end; ++G) {
     if (!SHIFTED) __syncthreads();                         // stage G landed
     const uint8_t *base = smem + (G & 3) * kStageBytes;
-    uint4 bf[4], af[kRows];
+    uint4 bf[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) bf[j] = *reinterpret_cast<const uint4 *>(base + b_off + j * 1024);
     const uint32_t sb = *reinterpret_cast<const uint32_t *>(base + sb_off);
-    // (of a 128-row tile the second word and strips 4.. are other rows', unused)
+    // (four strips or fewer: the second word is other rows', unused)
     const uint2 sa = make_uint2(*reinterpret_cast<const uint32_t *>(base + sa_off),
                                 *reinterpret_cast<const uint32_t *>(base + sa_off + 256));
-    af[0] = *reinterpret_cast<const uint4 *>(base + a_off);
-    af[1] = *reinterpret_cast<const uint4 *>(base + a_off + 1024);
-    if (!SHIFTED) {
-      strips<0, kRows, CHECK>(std::make_integer_sequence<int, kRows>{}, acc, bf, af, base + a_off,
-                              sb, sa, live);
+    if constexpr (LIVE == 0) {
+      some_strips(std::make_integer_sequence<int, kRows>{}, acc, bf, base + a_off, sb, sa, live);
+      if (SHIFTED) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __syncthreads();
+      }
     } else {
-      strips<0, kSplit, CHECK>(std::make_integer_sequence<int, kSplit>{}, acc, bf, af,
-                               base + a_off, sb, sa, live);
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // all of stage G read
-      __syncthreads();                                     // stage G + 1 landed
-      strips<kSplit, kSplit, CHECK>(std::make_integer_sequence<int, kRows - kSplit>{}, acc, bf, af,
-                                    base + a_off, sb, sa, live);
+      uint4 af[LIVE];
+      af[0] = *reinterpret_cast<const uint4 *>(base + a_off);
+      af[1] = *reinterpret_cast<const uint4 *>(base + a_off + 1024);
+      if (!SHIFTED) {
+        strips<0, LIVE, LIVE>(std::make_integer_sequence<int, LIVE>{}, acc, bf, af, base + a_off,
+                              sb, sa);
+      } else {
+        strips<0, kSplit, LIVE>(std::make_integer_sequence<int, kSplit>{}, acc, bf, af,
+                                base + a_off, sb, sa);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); // all of stage G read
+        __syncthreads();                                   // stage G + 1 landed
+        strips<kSplit, kSplit, LIVE>(std::make_integer_sequence<int, LIVE - kSplit>{}, acc, bf, af,
+                                     base + a_off, sb, sa);
+      }
     }
   }
 }
 
-// A multiplying wave's tiles.
-template <int F32, int MODE, int ACT, bool SHIFTED>
+// A multiplying wave's tiles; wave row 1 is the shifted one. The two differ in
+// their stages only: one copy of the epilogue, which is some 10 KB of code that
+// the first tile has to fetch.
+template <int F32, int MODE, int ACT>
 __device__ __forceinline__ void consume(const Plan &p, uint8_t *smem,
-                                        const int *ends, const int *units, int lane, int wn) {
-  constexpr int wm = SHIFTED ? 1 : 0;
+                                        const int *ends, const int *units, int lane, int wm, int wn) {
   uint8_t *slab = smem + kRing * kStageBytes + (wm * 4 + wn) * kSlab;
   float *columns = reinterpret_cast<float *>(smem + kColumns) + (wm * 4 + wn) * 64;
   const uint32_t b_off = (uint32_t)(kStageA + (wn * 4) * 1024 + lane * 16);
@@ -497,7 +527,7 @@ __device__ __forceinline__ void consume(const Plan &p, uint8_t *smem,
   for (int i = 0; i < kRows; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  if (SHIFTED) __syncthreads();                            // stage 0 landed
+  if (wm) __syncthreads();                                 // stage 0 landed
   int G = 0;
   for (int k = 0; k < p.mine; ++k) {
     int live, part;
@@ -510,10 +540,22 @@ __device__ __forceinline__ void consume(const Plan &p, uint8_t *smem,
       const int nk = __builtin_amdgcn_readfirstlane(t.nk);
       const uint32_t a_off = (uint32_t)(wm * part * 64 + lane * 16);
       const uint32_t sa_off = (uint32_t)(kStageA + kStageB) + wm * part * 4 + lane * 4;
-      if (live == kRows)
-        stages<SHIFTED, false>(acc, smem, G, nk, a_off, b_off, sa_off, sb_off, live);
-      else
-        stages<SHIFTED, true>(acc, smem, G, nk, a_off, b_off, sa_off, sb_off, live);
+      if (live == kRows) {
+        if (wm)
+          stages<true, kRows>(acc, smem, G, nk, a_off, b_off, sa_off, sb_off, live);
+        else
+          stages<false, kRows>(acc, smem, G, nk, a_off, b_off, sa_off, sb_off, live);
+      } else if (live == kRows / 2) {
+        if (wm)
+          stages<true, kRows / 2>(acc, smem, G, nk, a_off, b_off, sa_off, sb_off, live);
+        else
+          stages<false, kRows / 2>(acc, smem, G, nk, a_off, b_off, sa_off, sb_off, live);
+      } else {
+        if (wm)
+          stages<true, 0>(acc, smem, G, nk, a_off, b_off, sa_off, sb_off, live);
+        else
+          stages<false, 0>(acc, smem, G, nk, a_off, b_off, sa_off, sb_off, live);
+      }
       G += nk;
     }
     // the tile is looked up again: what it says would hold registers through
@@ -525,7 +567,7 @@ __device__ __forceinline__ void consume(const Plan &p, uint8_t *smem,
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
   }
-  if (!SHIFTED) __syncthreads();                           // the shifted waves' last barrier
+  if (!wm) __syncthreads();                                // the shifted waves' last barrier
 }
 
 template <int F32, int MODE, int ACT>
@@ -540,10 +582,7 @@ __global__ __launch_bounds__(kThreads, 1) void fused_tile_kernel(FusedArgs g) {
   }
   const Plan plan = make_plan(g, units);
   if (wave < kConsumers) {
-    if (wave >> 2)
-      consume<F32, MODE, ACT, true>(plan, smem, ends, units, lane, wave & 3);
-    else
-      consume<F32, MODE, ACT, false>(plan, smem, ends, units, lane, wave & 3);
+    consume<F32, MODE, ACT>(plan, smem, ends, units, lane, wave >> 2, wave & 3);
     return;
   }
 
