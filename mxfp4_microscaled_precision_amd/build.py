@@ -23,7 +23,8 @@ SOURCES = ["mx_quant.hip", "mx_gemm.hip", "mx_gemm_e4m3.hip", "mx_dequant.hip", 
            "mx_norm_dual.hip", "mx_norm_grad.hip", "mx_clip.hip", "mx_fused_small.hip",
            "mx_fused_tile.hip", "mx_fused_tile_f32.hip", "mx_fused_tile_bf16_grad.hip",
            "mx_fused_tile_f32_grad.hip", "mx_fused_tile_bf16_grad_mul.hip",
-           "mx_fused_tile_f32_grad_mul.hip", "mx_quant_grouped.hip", "mx_api.cpp"]
+           "mx_fused_tile_f32_grad_mul.hip", "mx_fused_tile_bf16_both.hip",
+           "mx_fused_tile_f32_both.hip", "mx_quant_grouped.hip", "mx_api.cpp"]
 
 # -ffp-contract=off: the rotation's adds and multiplies must round one by one.
 # -packed-fp32-ops off: packed fp32 VALU forms are not used by this library.

@@ -22,8 +22,10 @@
 namespace mx {
 
 // Direction of an epilogue, constant where the tile kernel's registers depend on
-// it: forward, or a gradient without and with mul.
-enum { kForward = 0, kGradient = 1, kGradientMul = 2 };
+// it: forward with at most one of mul and the residual, or with both; a gradient
+// without and with mul.
+enum { kForward = 0, kForwardBoth = 1, kGradient = 2, kGradientMul = 3 };
+constexpr bool is_gradient(int mode) { return mode >= kGradient; }
 
 constexpr float kLog2e = 1.44269504f;
 
@@ -153,7 +155,7 @@ __device__ __forceinline__ void epilogue_of(const float (&v)[N], M m, O o, bool 
                                             bool has_residual, float (&a)[N], float (&b)[N]) {
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    if (MODE != kForward) {
+    if (is_gradient(MODE)) {
       float slope;
       b[k] = v[k] * act_both<ACT>(o(k), slope);
       a[k] = v[k] * slope;
@@ -162,11 +164,11 @@ __device__ __forceinline__ void epilogue_of(const float (&v)[N], M m, O o, bool 
       a[k] = act_value<ACT>(v[k]);
     }
   }
-  if (MODE == kGradientMul || (MODE == kForward && has_mul)) {
+  if (MODE == kGradientMul || (!is_gradient(MODE) && has_mul)) {
 #pragma unroll
     for (int k = 0; k < N; ++k) a[k] *= m(k);
   }
-  if (MODE == kForward && has_residual) {
+  if (!is_gradient(MODE) && has_residual) {
 #pragma unroll
     for (int k = 0; k < N; ++k) a[k] += o(k);
   }
@@ -180,7 +182,7 @@ __device__ __forceinline__ void epilogue_unit(const float (&v)[kUnit<F32>], bool
                                               bool has_residual, const row_u32x4 &mul,
                                               const row_u32x4 &other, row_u32x4 &c,
                                               row_u32x4 &second) {
-  constexpr int n = MODE == kForward ? 4 : 2;
+  constexpr int n = is_gradient(MODE) ? 2 : 4;
 #pragma unroll
   for (int i = 0; i < kUnit<F32>; i += n) {
     float x[n], a[n], b[n];
@@ -191,7 +193,7 @@ __device__ __forceinline__ void epilogue_unit(const float (&v)[kUnit<F32>], bool
         [&](int k) { return unit_element<F32>(other, i + k); }, has_mul, has_residual, a, b);
     unit_put<F32>(second, i, b);
     unit_put<F32>(c, i, a);
-    if (MODE != kForward) __builtin_amdgcn_sched_barrier(0);
+    if (is_gradient(MODE)) __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -210,7 +212,7 @@ __device__ __forceinline__ void epilogue8(const float (&v)[8], const float (&bia
       epilogue_unit<F32, kGradient, ACT>(x, false, false, mul.w[h], other.w[h], c.w[h],
                                          second.w[h]);
     else
-      epilogue_unit<F32, GRAD ? kGradientMul : kForward, ACT>(
+      epilogue_unit<F32, GRAD ? kGradientMul : kForwardBoth, ACT>(
           x, has_mul, has_residual, mul.w[h], other.w[h], c.w[h], second.w[h]);
   }
 }

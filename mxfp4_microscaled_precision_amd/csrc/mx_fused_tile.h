@@ -319,19 +319,23 @@ struct Rows {
 // pair p: eight instructions a strip, where staging rows of 64 columns in LDS took
 // some 260 and most of the epilogue's time.
 //
-// mul and the residual of a unit are asked for one unit ahead at first and up to
-// four once the accumulators of finished units leave registers for them; each
+// mul, the residual or pre of a unit are asked for one unit ahead at first, and
+// further once the accumulators of finished units leave registers for them; each
 // request goes out before its unit's stores, so that no load waits for a store.
 template <int F32, int MODE, int ACT>
 __device__ __forceinline__ void finish_rows(const FusedArgs &g, const Tile &t,
                                             const v4f (&acc)[kRows][4], const float *columns,
                                             int64_t c_row, int row0, int col0, int live, int lane) {
-  constexpr bool GRAD = MODE != kForward;
+  constexpr bool GRAD = is_gradient(MODE);
   constexpr int kSize = F32 ? 4 : 2, n = kUnit<F32>;
   constexpr int kPerStrip = F32 ? 4 : 2;           // units of a lane in a strip
-  constexpr int kUnits = kPerStrip * kRows, kSlots = 5;
-  const Rows pm(g.e.mul, g.e.ldmul, c_row + row0, col0, kSize);
-  const Rows po(other_of<GRAD>(g.e), other_ld<GRAD>(g.e), c_row + row0, col0, kSize);
+  constexpr int kUnits = kPerStrip * kRows;
+  // two matrices to read, or one (which a forward call chooses)
+  constexpr bool TWO = MODE == kForwardBoth || MODE == kGradientMul;
+  const bool gate = !GRAD && g.e.mul;
+  const Rows pm(TWO ? g.e.mul : nullptr, g.e.ldmul, c_row + row0, col0, kSize);
+  const Rows po(!TWO && gate ? g.e.mul : other_of<GRAD>(g.e),
+                !TWO && gate ? g.e.ldmul : other_ld<GRAD>(g.e), c_row + row0, col0, kSize);
   const Rows p2(second_of<GRAD>(g.e), second_ld<GRAD>(g.e), c_row + row0, col0, kSize);
   const Rows pc(g.c, g.ldc, c_row + row0, col0, kSize);
   // Byte of this lane in a strip of matrix m: one multiply-add, made anew at every
@@ -346,19 +350,21 @@ __device__ __forceinline__ void finish_rows(const FusedArgs &g, const Tile &t,
     asm volatile("v_mad_u32_u24 %0, %1, %2, %3" : "=v"(b) : "v"(lr), "s"(m.pitch), "v"(c0));
     return lr + (uint32_t)(16 * i - before) < (uint32_t)count ? b : kOutside;
   };
-  // the last unit asked for when unit u is done
-  constexpr int kWait = GRAD ? 4 * kPerStrip / 2 : kPerStrip, kSlow = F32 ? 4 : GRAD ? 3 : 2;
+  // the last unit asked for when unit u is done: kMost units ahead at most
+  constexpr int kMost = TWO ? 4 : 10, kSlots = kMost + 1;
+  constexpr int kWait = GRAD ? 2 * kPerStrip : kPerStrip;
+  constexpr int kSlow = (F32 ? 2 : 1) * (TWO ? GRAD ? 3 : 2 : 1);
   constexpr auto requested = [](int u) {
     const int more = u < kWait ? 0 : (u - kWait) / kSlow;
-    return u + 1 + (more < 3 ? more : 3);
+    return u + 1 + (more < kMost - 1 ? more : kMost - 1);
   };
-  row_u32x4 mul[kSlots], other[kSlots];
+  row_u32x4 mul[TWO ? kSlots : 1], other[kSlots];
   auto load = [&](auto unit) {
     constexpr int u = unit();
     constexpr int i = u / kPerStrip, byte = (u % kPerStrip) * 64;
     if (u >= kUnits || i >= live) return;
-    if (GRAD ? MODE == kGradientMul : pm.any) mul[u % kSlots] = pm.load(at(pm, i), 16 * i, byte);
-    if (GRAD || po.any) other[u % kSlots] = po.load(at(po, i), 16 * i, byte);
+    if constexpr (TWO) mul[u % kSlots] = pm.load(at(pm, i), 16 * i, byte);
+    if (TWO || GRAD || po.any) other[u % kSlots] = po.load(at(po, i), 16 * i, byte);
   };
   load(std::integral_constant<int, 0>());
   for_each_int<kUnits>([&](auto unit) {
@@ -386,8 +392,9 @@ __device__ __forceinline__ void finish_rows(const FusedArgs &g, const Tile &t,
         }
       }
       row_u32x4 c, second;
-      epilogue_unit<F32, MODE, ACT>(v, pm.any, po.any, mul[u % kSlots], other[u % kSlots], c,
-                                    second);
+      epilogue_unit<F32, MODE, ACT>(v, TWO || gate, TWO || (po.any && !gate),
+                                    TWO ? mul[TWO ? u % kSlots : 0] : other[u % kSlots],
+                                    other[u % kSlots], c, second);
       __builtin_amdgcn_sched_barrier(0);
       constexpr int done = u == 0 ? 0 : requested(u - 1), more = requested(u) - done;
       load(std::integral_constant<int, done + 1>());
@@ -410,7 +417,7 @@ __device__ __forceinline__ void finish_columns(const FusedArgs &g, const Tile &t
                                                const v4f (&acc)[kRows][4], uint8_t *slab,
                                                const float *columns, int64_t c_row, int row0,
                                                int col0, int live, int lane) {
-  constexpr bool GRAD = MODE != kForward;
+  constexpr bool GRAD = is_gradient(MODE);
 #pragma clang loop unroll(disable)
   for (int s = 0; s < 4 * live; ++s) {             // four rows, half s % 2 of eight
     int l = lane;
@@ -676,6 +683,8 @@ hipError_t launch_tiles(const FusedArgs &g, dim3 grid, hipStream_t stream) {
 
 // (each in a source file of its own, so that they compile side by side)
 hipError_t launch_tiles_bf16(const FusedArgs &g, dim3 grid, hipStream_t stream);
+hipError_t launch_tiles_bf16_both(const FusedArgs &g, dim3 grid, hipStream_t stream);
+hipError_t launch_tiles_f32_both(const FusedArgs &g, dim3 grid, hipStream_t stream);
 hipError_t launch_tiles_f32(const FusedArgs &g, dim3 grid, hipStream_t stream);
 hipError_t launch_tiles_bf16_grad(const FusedArgs &g, dim3 grid, hipStream_t stream);
 hipError_t launch_tiles_f32_grad(const FusedArgs &g, dim3 grid, hipStream_t stream);

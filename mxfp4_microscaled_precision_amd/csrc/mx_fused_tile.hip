@@ -31,6 +31,9 @@ static hipError_t fused_tile_launch(FusedArgs g, hipStream_t stream) {
   if (g.grad)
     return g.out_bf16 ? launch_tiles_bf16_grad(g, grid, stream)
                       : launch_tiles_f32_grad(g, grid, stream);
+  if (g.e.mul && g.e.residual)
+    return g.out_bf16 ? launch_tiles_bf16_both(g, grid, stream)
+                      : launch_tiles_f32_both(g, grid, stream);
   return g.out_bf16 ? launch_tiles_bf16(g, grid, stream) : launch_tiles_f32(g, grid, stream);
 }
 

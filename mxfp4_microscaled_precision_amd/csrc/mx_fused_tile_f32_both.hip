@@ -1,0 +1,10 @@
+// The tile kernel's instances for fp32 outputs with a gate and a residual.
+#include "mx_fused_tile.h"
+
+namespace mx {
+
+hipError_t launch_tiles_f32_both(const FusedArgs &g, dim3 grid, hipStream_t stream) {
+  return tile::launch_tiles<1, kForwardBoth>(g, grid, stream);
+}
+
+}  // namespace mx
