@@ -678,7 +678,7 @@ mx_status mx_quantize_grouped_workspace(int64_t rows, int64_t cols, int32_t grou
  *             == NULL for none (desc0 is then not written).
  *  sums       device fp32 [groups, cols], 4-byte aligned: each group's column
  *             sums (what the bias of a linear whose output gradient x is
- *             gets), summed in fp32, 32 rows at a time; or NULL.
+ *             gets), summed in fp32, 128 rows at a time; or NULL.
  *  workspace  device, >= mx_quantize_grouped_workspace bytes, 16-byte aligned
  *             (with sums only; as for mx_rmsnorm_backward).
  * The descriptors may be NULL. rows == 0 writes zeros to sums; cols == 0

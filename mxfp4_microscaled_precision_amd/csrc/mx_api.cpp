@@ -988,8 +988,8 @@ mx_status mx_quantize_grouped_workspace(int64_t rows, int64_t cols, int32_t grou
   const mx_status st =
       grouped_sizes(rows, cols, groups, group_rows, MX_AXIS_GROUPED, &c, &s);
   if (st != MX_OK) return st;
-  // a row of partial sums per 32-deep block
-  *bytes = rows == 0 ? 0 : (size_t)grouped_slices(rows, groups, group_rows) * 4 * (size_t)cols * 4;
+  // a row of partial sums per slice
+  *bytes = rows == 0 ? 0 : (size_t)grouped_slices(rows, groups, group_rows) * (size_t)cols * 4;
   return MX_OK;
 }
 
@@ -1073,6 +1073,10 @@ mx_status mx_quantize_grouped(const mx_grouped_source *source, int32_t block, in
   a.scales1 = static_cast<uint8_t *>(scales1);
   a.codes0 = static_cast<uint8_t *>(codes0);
   a.scales0 = static_cast<uint8_t *>(scales0);
+  if (x.src_rows == 0) {           // every row is one of zeros; its loads need memory all the same
+    a.x = static_cast<const uint16_t *>(codes1);
+    a.ld = 0;
+  }
   a.partial = sums != nullptr ? static_cast<float *>(workspace) : nullptr;
   a.sums = sums;
   return hip_status(mx::quantize_grouped_launch(a, static_cast<hipStream_t>(stream)));

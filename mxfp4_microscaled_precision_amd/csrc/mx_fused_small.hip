@@ -3,7 +3,7 @@
 //
 // With few rows a product is bound by reading the weights once, and a 256-wide
 // tile per compute unit would leave most of the card idle. Here a workgroup
-// takes 64 columns of 16 or 64 rows and splits the reduction over its waves:
+// takes 64 or 16 columns of 64 or 16 rows and splits the reduction over its waves:
 // wave w reads slices w, w + W, .. straight from memory into registers (a
 // tile of the layout is one contiguous 1 KB load of 16 bytes per lane, which
 // is the matrix instruction's fragment), and the waves' sums meet in LDS,
@@ -24,21 +24,18 @@ namespace {
 
 using namespace gemm;
 
-constexpr int kWaves = 8;
-constexpr int kCols = 64;                          // columns of a workgroup's tile
-constexpr int kPitch = kCols + 4;                  // LDS row of fp32 sums, 16 bytes of padding
-
-// What a wave reads of one 128-deep slice: R row groups of A, four of B, and
-// the scales of the four row groups that each sits among.
-template <int R>
+// What a wave reads of one 128-deep slice: R row groups of A, J of B (four or
+// one), and the scales of the four row groups that each sits among.
+template <int R, int J>
 struct Slice {
-  uint4 a[R], b[4];
+  uint4 a[R], b[J];
   uint32_t sa, sb;
 };
 
-template <int R, int F32, bool GRAD>
+template <int R, int J, int kWaves, int F32, bool GRAD>
 __global__ __launch_bounds__(64 * kWaves) void fused_small_kernel(FusedArgs g, int row_tiles) {
-  constexpr int kRows = 16 * R;
+  constexpr int kRows = 16 * R, kCols = 16 * J;
+  constexpr int kPitch = kCols + 4;                // LDS row of fp32 sums, 16 bytes of padding
   __shared__ __attribute__((aligned(16))) float red[kWaves][kRows][kPitch];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -77,11 +74,11 @@ __global__ __launch_bounds__(64 * kWaves) void fused_small_kernel(FusedArgs g, i
   }
   if (col0 >= g.N) return;
 
-  v4f acc[R][4];
+  v4f acc[R][J];
 #pragma unroll
   for (int i = 0; i < R; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < J; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
   const int ga = ra >> 4, gb = rb >> 4;
   const uint8_t *pa = g.a_codes + ((int64_t)ga * g.a_slices + ka) * 1024 + lane * 16;
   const uint8_t *pb = g.b_codes + ((int64_t)gb * g.b_slices + kb) * 1024 + lane * 16;
@@ -89,9 +86,9 @@ __global__ __launch_bounds__(64 * kWaves) void fused_small_kernel(FusedArgs g, i
                       ((ga >> 2) & 3) * 256 + lane * 4;
   const uint8_t *qb = g.b_scales + ((int64_t)kb * g.b_panels + (gb >> 4)) * 1024 +
                       ((gb >> 2) & 3) * 256 + lane * 4;
-  auto read = [&](Slice<R> &s, int k) {
+  auto read = [&](Slice<R, J> &s, int k) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < J; ++j)
       s.b[j] = *reinterpret_cast<const uint4 *>(pb + ((int64_t)j * g.b_slices + k) * 1024);
 #pragma unroll
     for (int i = 0; i < R; ++i)
@@ -99,25 +96,24 @@ __global__ __launch_bounds__(64 * kWaves) void fused_small_kernel(FusedArgs g, i
     s.sb = *reinterpret_cast<const uint32_t *>(qb + (int64_t)k * g.b_panels * 1024);
     s.sa = *reinterpret_cast<const uint32_t *>(qa + (int64_t)k * g.a_panels * 1024);
   };
-  auto multiply = [&](const Slice<R> &s) {
+  auto multiply = [&](const Slice<R, J> &s) {
     // one row group: its byte of the four comes to the front
     const uint32_t sa = R == 1 ? s.sa >> (8 * (ga & 3)) : s.sa;
+    const uint32_t sb = J == 1 ? s.sb >> (8 * (gb & 3)) : s.sb;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      // (the byte select is part of the instruction)
-#define MX_ROW(I)                                                              \
-  if (i == I) {                                                                \
-    acc[i][0] = mfma_fp4<0, I>(s.b[0], s.a[i], acc[i][0], s.sb, sa);           \
-    acc[i][1] = mfma_fp4<1, I>(s.b[1], s.a[i], acc[i][1], s.sb, sa);           \
-    acc[i][2] = mfma_fp4<2, I>(s.b[2], s.a[i], acc[i][2], s.sb, sa);           \
-    acc[i][3] = mfma_fp4<3, I>(s.b[3], s.a[i], acc[i][3], s.sb, sa);           \
-  }
+      // (the byte selects are part of the instruction)
+#define MX_TILE(I, K)                                                                  \
+  if constexpr (K < J)                                                                 \
+    if (i == I) acc[i][K] = mfma_fp4<K, I>(s.b[K], s.a[i], acc[i][K], sb, sa);
+#define MX_ROW(I) MX_TILE(I, 0) MX_TILE(I, 1) MX_TILE(I, 2) MX_TILE(I, 3)
       MX_ROW(0) MX_ROW(1) MX_ROW(2) MX_ROW(3)
 #undef MX_ROW
+#undef MX_TILE
     }
   };
   // two slices ahead of the one that is multiplied
-  Slice<R> s0, s1;
+  Slice<R, J> s0, s1;
   int k = wave;
   if (k < nk) read(s0, k);
   for (; k < nk; k += 2 * kWaves) {
@@ -131,76 +127,132 @@ __global__ __launch_bounds__(64 * kWaves) void fused_small_kernel(FusedArgs g, i
 #pragma unroll
   for (int i = 0; i < R; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < J; ++j)
       *reinterpret_cast<v4f *>(&red[wave][16 * i + lr][16 * j + 4 * lg]) = acc[i][j];
 
-  // thread -> eight columns of one row
-  const int row = ra + (tid >> 3), c8 = (tid & 7) * 8, col = col0 + c8;
-  const int lo = max(0, -col), hi = min(8, g.N - col);
-  const bool live = tid < kRows * 8 && row >= first && row < last && lo < hi;
-  const bool vec = g.e.vec && lo == 0 && hi == 8 && (col & 7) == 0;
-  Row8<F32> mul, other, c, second;
-  float bias[8];
-  if (live) {
-    if (g.e.mul) mul = load_cols<F32>(g.e.mul, (c_row + row) * g.e.ldmul + col, vec, lo, hi);
-    if (other_of<GRAD>(g.e))
-      other = load_cols<F32>(other_of<GRAD>(g.e), (c_row + row) * other_ld<GRAD>(g.e) + col, vec,
-                             lo, hi);
+  // A lane has eight columns of a row, where every matrix takes 16-byte accesses;
+  // else one column of four rows, so that the lanes still access adjacent columns.
+  const bool vec = g.e.vec && col0 >= 0 && col0 + kCols <= g.N && (col0 & 7) == 0;
+  if (vec) {
+    constexpr int kUnits = kCols / 8, kStep = 64 / kUnits;        // rows of a wave at a time
+    __syncthreads();
+#pragma unroll 1
+    for (int r8 = wave * kStep; r8 < kRows; r8 += kStep * kWaves) {
+      const int r = r8 + lane / kUnits, c8 = lane % kUnits * 8, row = ra + r, col = col0 + c8;
+      if (r >= kRows || row < first || row >= last) continue;
+      const int64_t at = c_row + row;
+      Row8<F32> mul, other, c, second;
+      if (g.e.mul) mul = load8<F32>(g.e.mul, at * g.e.ldmul + col);
+      if (other_of<GRAD>(g.e)) other = load8<F32>(other_of<GRAD>(g.e), at * other_ld<GRAD>(g.e) + col);
+      float v[8], bias[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      bias[i] = g.e.bias && i >= lo && i < hi ? load_bias(g.e, (int64_t)e * g.N + col + i) : 0.0f;
+      for (int i = 0; i < 8; ++i) {
+        v[i] = 0.0f;
+        bias[i] = !GRAD && g.e.bias ? load_bias(g.e, (int64_t)e * g.N + col + i) : 0.0f;
+      }
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const v4f d = *reinterpret_cast<const v4f *>(&red[w][r][c8 + 4 * h]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[4 * h + i] += d[i];
+        }
+      }
+      with_act(g.e.act, [&](auto act) {
+        epilogue8<F32, GRAD, act()>(v, bias, g.e.mul, g.e.residual, mul, other, c, second);
+      });
+      if (second_of<GRAD>(g.e)) store8<F32>(second_of<GRAD>(g.e), at * second_ld<GRAD>(g.e) + col, second);
+      store8<F32>(g.c, at * g.ldc + col, c);
+    }
+    return;
   }
+  const int mine = lane % kCols, col = col0 + mine;
+  const bool in = col >= 0 && col < g.N;
+  const float bias = !GRAD && g.e.bias && in ? load_bias(g.e, (int64_t)e * g.N + col) : 0.0f;
   __syncthreads();
-  if (!live) return;
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (!in) return;
+#pragma unroll 1
+  for (int r4 = (wave * (64 / kCols) + lane / kCols) * 4; r4 < kRows;
+       r4 += 4 * (64 / kCols) * kWaves) {
+    float v[4], m[4], o[4], a[4], b[4];
+    const void *const from = other_of<GRAD>(g.e);
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    const float *p = &red[w][tid >> 3][c8];
+    for (int i = 0; i < 4; ++i) {
+      const int row = ra + r4 + i;
+      const bool mine = row >= first && row < last;
+      m[i] = mine && g.e.mul ? load_one<F32>(g.e.mul, (c_row + row) * g.e.ldmul + col) : 0.0f;
+      o[i] = mine && from ? load_one<F32>(from, (c_row + row) * other_ld<GRAD>(g.e) + col) : 0.0f;
+      v[i] = 0.0f;
+    }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const v4f d = *reinterpret_cast<const v4f *>(p + 4 * h);
+    for (int w = 0; w < kWaves; ++w)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[4 * h + i] += d[i];
+      for (int i = 0; i < 4; ++i) v[i] += red[w][r4 + i][mine];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += bias;
+    with_act(g.e.act, [&](auto act) {
+      auto mul = [&](int k) { return m[k]; };
+      auto other = [&](int k) { return o[k]; };
+      if (GRAD && !g.e.mul)
+        epilogue_of<kGradient, act()>(v, mul, other, false, false, a, b);
+      else
+        epilogue_of<GRAD ? kGradientMul : kForwardBoth, act()>(v, mul, other, g.e.mul,
+                                                               g.e.residual, a, b);
+    });
+    void *const to2 = second_of<GRAD>(g.e);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = ra + r4 + i;
+      if (row < first || row >= last) continue;
+      if (to2) store_one<F32>(to2, (c_row + row) * second_ld<GRAD>(g.e) + col, b[i]);
+      store_one<F32>(g.c, (c_row + row) * g.ldc + col, a[i]);
     }
   }
-  with_act(g.e.act, [&](auto act) {
-    epilogue8<F32, GRAD, act()>(v, bias, g.e.mul, g.e.residual, mul, other, c, second);
-  });
-  if (second_of<GRAD>(g.e))
-    store_cols<F32>(second_of<GRAD>(g.e), (c_row + row) * second_ld<GRAD>(g.e) + col, vec, lo, hi,
-                    second);
-  store_cols<F32>(g.c, (c_row + row) * g.ldc + col, vec, lo, hi, c);
 }
 
-template <int R, int F32, bool GRAD>
+// Tiles of `rows` rows and of `cols` columns, at most.
+int64_t count_row_tiles(const FusedArgs &g, int rows) {
+  const int64_t tm = ((int64_t)g.M + rows - 1) / rows;
+  if (g.kind == MX_K_WGRAD) return tm * g.groups;
+  // a group's tiles begin at a multiple of `rows`: up to two more than its rows'
+  return g.ends ? g.rows / rows + 2 * (int64_t)std::min(g.groups, g.rows) : tm;
+}
+
+int64_t count_col_tiles(const FusedArgs &g, int cols) {
+  const int64_t ct = ((int64_t)g.N + cols - 1) / cols;
+  return ct + (g.kind == MX_K_FPROP && g.groups > 1 && g.N % cols ? 1 : 0);   // any first column
+}
+
+template <int R, int J, int W, int F32, bool GRAD>
 hipError_t launch_small(const FusedArgs &g, hipStream_t stream) {
-  constexpr int kRows = 16 * R;
-  const int64_t tm = ((int64_t)g.M + kRows - 1) / kRows;
-  // a group's tiles begin at a multiple of kRows: up to two more than its rows'
-  int64_t rt = tm;
-  if (g.kind == MX_K_WGRAD)
-    rt = tm * g.groups;
-  else if (g.ends)
-    rt = g.rows / kRows + 2 * (int64_t)std::min(g.groups, g.rows);
-  int64_t ct = ((int64_t)g.N + kCols - 1) / kCols;
-  if (g.kind == MX_K_FPROP && g.groups > 1 && g.N % kCols) ++ct;   // unaligned first columns
+  const int64_t rt = count_row_tiles(g, 16 * R), ct = count_col_tiles(g, 16 * J);
   if (rt * ct == 0) return hipSuccess;
   if (rt * ct > INT32_MAX) return hipErrorInvalidValue;
-  return launch(fused_small_kernel<R, F32, GRAD>, dim3((unsigned)(rt * ct)), dim3(64 * kWaves), 0,
+  return launch(fused_small_kernel<R, J, W, F32, GRAD>, dim3((unsigned)(rt * ct)), dim3(64 * W), 0,
                 stream, g, (int)rt);
 }
 
-template <int R>
-hipError_t launch_rows(const FusedArgs &g, hipStream_t stream) {
+template <int R, int J, int W>
+hipError_t launch_tile(const FusedArgs &g, hipStream_t stream) {
   if (g.grad)
-    return g.out_bf16 ? launch_small<R, 0, true>(g, stream) : launch_small<R, 1, true>(g, stream);
-  return g.out_bf16 ? launch_small<R, 0, false>(g, stream) : launch_small<R, 1, false>(g, stream);
+    return g.out_bf16 ? launch_small<R, J, W, 0, true>(g, stream)
+                      : launch_small<R, J, W, 1, true>(g, stream);
+  return g.out_bf16 ? launch_small<R, J, W, 0, false>(g, stream)
+                    : launch_small<R, J, W, 1, false>(g, stream);
 }
 
 }  // namespace
 
 hipError_t fused_small_launch(const FusedArgs &g, hipStream_t stream) {
-  return g.M <= 16 ? launch_rows<1>(g, stream) : launch_rows<4>(g, stream);
+  const int64_t cus = cu_count();
+  const int rows = g.kind == MX_K_WGRAD ? g.M : g.rows / g.groups;   // of a group, on average
+  // workgroups of 64 columns on less than half of the card: 16 columns each
+  const int64_t tiles = count_row_tiles(g, rows <= 16 ? 16 : 64) * count_col_tiles(g, 64);
+  if (rows <= 16)
+    return 2 * tiles <= cus ? launch_tile<1, 1, 8>(g, stream) : launch_tile<1, 4, 8>(g, stream);
+  if (4 * tiles <= cus) return launch_tile<4, 1, 8>(g, stream);
+  return tiles <= cus ? launch_tile<4, 4, 8>(g, stream) : launch_tile<4, 4, 4>(g, stream);
 }
 
 }  // namespace mx

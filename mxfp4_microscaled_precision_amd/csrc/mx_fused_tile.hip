@@ -37,10 +37,17 @@ static hipError_t fused_tile_launch(FusedArgs g, hipStream_t stream) {
   return g.out_bf16 ? launch_tiles_bf16(g, grid, stream) : launch_tiles_f32(g, grid, stream);
 }
 
+// The kernel of few rows, where its 64x64 tiles (about one more per group than its
+// rows fill) go round the compute units twice at most: a 256-wide tile's stages
+// and epilogue then take longer than all of them. Measured with SiLU, us (few
+// rows / tiles): 512x4096x4096 16.6 / 22.4, 128x14336x4096 15.6 / 23.5,
+// 2048x1024x4096 12.1 / 21.9; 1024x4096x4096 25.8 / 23.3, 256x14336x4096 26.7 / 23.4.
 hipError_t fused_launch(const FusedArgs &g, hipStream_t stream) {
-  const int64_t rows = g.kind == MX_K_WGRAD ? g.M : g.rows / g.groups;   // of a group, on average
-  return g.groups > tile::kTileGroups || rows <= 64 ? fused_small_launch(g, stream)
-                                              : fused_tile_launch(g, stream);
+  const int64_t rows = g.kind == MX_K_WGRAD ? (int64_t)g.groups * ((g.M + 63) / 64)
+                       : (g.rows + 63) / 64 + (g.ends ? std::min(g.groups, g.rows) : 0);
+  const bool few = rows * (((int64_t)g.N + 63) / 64) <= 2 * (int64_t)cu_count();
+  return few || g.groups > tile::kTileGroups ? fused_small_launch(g, stream)
+                                             : fused_tile_launch(g, stream);
 }
 
 }  // namespace mx

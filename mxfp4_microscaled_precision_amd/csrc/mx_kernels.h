@@ -167,7 +167,7 @@ struct GroupedQuantArgs {
   uint32_t seed1_lo, seed1_hi, seed0_lo, seed0_hi;
   uint8_t *codes1, *scales1;
   uint8_t *codes0, *scales0;       // or null
-  float *partial, *sums;           // [4 slices][cols], [groups][cols], or null
+  float *partial, *sums;           // [slices][cols], [groups][cols], or null
 };
 
 hipError_t quantize_grouped_launch(const GroupedQuantArgs &a, hipStream_t stream);

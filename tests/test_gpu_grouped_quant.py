@@ -137,6 +137,18 @@ def test_empty(mx):
     assert q.sums.shape == (2, 0)
 
 
+def test_no_source_rows(mx):
+    """An index into nothing: rows of zeros."""
+    import torch
+    x = torch.empty((0, 96), dtype=torch.bfloat16, device="cuda")
+    for dual in (True, False):
+        q = mx.quantize_grouped(x, _ends([3, 150]), sums=dual, dual=dual,
+                                index=torch.arange(200, device="cuda", dtype=torch.int32))
+        _check(q, np.zeros((200, 96), np.uint16), oracle.group_ranges_ref([3, 153], 200), -1,
+               "hadamard", "rne", (0, 0), dual)
+        assert not dual or not q.sums.any()
+
+
 def test_same_bytes_as_the_single_quantizers(mx):
     """Groups of whole slices: the dual quantizer's operands, slice by slice."""
     rng = np.random.Generator(np.random.PCG64(12))
