@@ -37,17 +37,22 @@ static hipError_t fused_tile_launch(FusedArgs g, hipStream_t stream) {
   return g.out_bf16 ? launch_tiles_bf16(g, grid, stream) : launch_tiles_f32(g, grid, stream);
 }
 
-// The kernel of few rows, where its 64x64 tiles (about one more per group than its
-// rows fill) go round the compute units twice at most: a 256-wide tile's stages
-// and epilogue then take longer than all of them. Measured with SiLU, us (few
-// rows / tiles): 512x4096x4096 16.6 / 22.4, 128x14336x4096 15.6 / 23.5,
-// 2048x1024x4096 12.1 / 21.9; 1024x4096x4096 25.8 / 23.3, 256x14336x4096 26.7 / 23.4.
+// The kernel of few rows where its 64x64 tiles (about one more per group than its
+// rows fill) go round the compute units three times at most, or four where accesses
+// are narrow: a 256-wide tile's stages and epilogue then take longer than all of
+// them. And where a group has a handful of rows on average: what counts is then that
+// its weights are read once. Measured, us (few rows / tiles): with SiLU, 512x4096x4096
+// 16.6 / 22.4, 128x14336x4096 15.6 / 23.5, 2048x1024x4096 12.1 / 21.9, and past the
+// limit 1024x4096x4096 25.8 / 23.3, 256x14336x4096 26.7 / 23.4; fp32 rows of 1001
+// columns, 4000x1001x1024 19.1 / 41.0; 256 rows of 8 experts 4096x4096 25.2 / 29.7,
+// of 64 experts 2048x1024 18.3 / 21.5, 4096 rows of those 45.7 / 27.6.
 hipError_t fused_launch(const FusedArgs &g, hipStream_t stream) {
   const int64_t rows = g.kind == MX_K_WGRAD ? (int64_t)g.groups * ((g.M + 63) / 64)
                        : (g.rows + 63) / 64 + (g.ends ? std::min(g.groups, g.rows) : 0);
-  const bool few = rows * (((int64_t)g.N + 63) / 64) <= 2 * (int64_t)cu_count();
-  return few || g.groups > tile::kTileGroups ? fused_small_launch(g, stream)
-                                             : fused_tile_launch(g, stream);
+  const bool few = rows * (((int64_t)g.N + 63) / 64) <= (g.e.vec ? 3 : 4) * (int64_t)cu_count();
+  const bool handful = g.kind != MX_K_WGRAD && g.rows / g.groups <= 8;
+  return few || handful || g.groups > tile::kTileGroups ? fused_small_launch(g, stream)
+                                                        : fused_tile_launch(g, stream);
 }
 
 }  // namespace mx
