@@ -1,0 +1,226 @@
+"""Products with an epilogue and grouped ones, of sizes with enough 64x64 tiles
+(more than three a compute unit) for the kernel of 256x256 tiles: tiles cut by
+the matrix's ends, halves of tiles, several tiles a workgroup, matrices read and
+written by columns, groups that end inside a tile. Against fp64."""
+import numpy as np
+import pytest
+
+import oracle
+from datagen import activations_bf16, normal_bf16
+from fused_util import check, check_backward, check_forward, host64, product, values
+from gpu_util import to_dev
+from test_gpu_fused import _grouped_ref, _pair, _rows
+
+pytestmark = pytest.mark.gpu
+
+# N of whole 16-byte units, of 4-element ones only (fp32: whole, bf16: not), odd
+SHAPES = [(1100, 3136, 160), (1290, 3204, 96), (1100, 3905, 288)]
+WAYS = [("none", "b"), ("relu", "bm"), ("silu", "br"), ("gelu", "mr"), ("gelu_tanh", "bmr"),
+        ("silu", "m"), ("none", "r"), ("gelu", "")]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape,op", zip(SHAPES, ["fprop", "dgrad", "wgrad"]))
+def test_forward(mx, shape, op, dtype):
+    m, n, k = shape
+    qa, qb, acc, err = _pair(mx, m + n, op, m, n, k)
+    bias, mul, res = _rows(1, (n,), "f32"), _rows(2, (m, n), dtype), _rows(3, (m, n), dtype)
+    for i, (act, what) in enumerate(WAYS):
+        b, u, r = (x if c in what else None for c, x in zip("bmr", (bias, mul, res)))
+        got = mx.linear_fused(op, qa, qb, out_dtype=dtype, bias=b, activation=act, mul=u,
+                              residual=r, save_pre=i % 2 == 0)
+        c, pre = got if i % 2 == 0 else (got, None)
+        check_forward(c, pre, acc, err, dtype, act, host64(b), host64(u), host64(r), f"{act} {what}")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_backward(mx, shape, dtype):
+    import torch
+    m, n, k = shape
+    qa, qb, acc, err = _pair(mx, m * n, "dgrad", m, n, k)
+    pre, mul = _rows(4, (m, n), dtype), _rows(5, (m, n), dtype)
+    for i, act in enumerate(("none", "relu", "silu", "gelu", "gelu_tanh")):
+        u = mul if i % 2 else None
+        got = mx.linear_act_backward(qa, qb, pre, act, mul=u, out_dtype=dtype)
+        dz, dmul = got if u is not None else (got, None)
+        check_backward(dz, dmul, acc, err, host64(pre), dtype, act, host64(u), act)
+    dz, dmul = mx.linear_act_backward(qa, qb, pre, "silu", mul=mul, out_dtype=dtype, out=pre, dmul=mul)
+    assert torch.equal(dz, mx.linear_act_backward(qa, qb, _rows(4, (m, n), dtype), "silu",
+                                                  mul=_rows(5, (m, n), dtype), out_dtype=dtype)[0])
+
+
+@pytest.mark.parametrize("op,act", [("fprop", "silu"), ("wgrad", "gelu")])
+def test_several_tiles_a_workgroup(mx, op, act):
+    """More than 256 tiles of 256x256, the last round of them cut in halves."""
+    m, n, k = 4200, 4352, 64
+    qa, qb, acc, err = _pair(mx, 3, op, m, n, k)
+    mul = _rows(2, (m, n), "bf16")
+    c, pre = mx.linear_fused(op, qa, qb, out_dtype="bf16", activation=act, mul=mul, save_pre=True)
+    check_forward(c, pre, acc, err, "bf16", act, None, host64(mul), None, "large")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_strided_and_misaligned_matrices(mx, dtype):
+    """Row-strided views at odd addresses; what lies between the rows stays."""
+    import torch
+    m, n, k = 1250, 3600, 160
+    qa, qb, acc, err = _pair(mx, 9, "fprop", m, n, k)
+    mul, res = _rows(6, (m, n), dtype, n + 9), _rows(7, (m, n), dtype, n + 3)
+    bias = _rows(8, (n + 1,), "bf16")[1:]
+    buf = torch.full((2, m, n + 5), 7.0, device="cuda").to(mul.dtype)
+    out, pre = buf[0, :, 1:n + 1], buf[1, :, 3:n + 3]
+    mx.linear_fused("fprop", qa, qb, out_dtype=dtype, bias=bias, activation="silu", mul=mul,
+                    residual=res, save_pre=pre, out=out)
+    check_forward(out, pre, acc, err, dtype, "silu", host64(bias), host64(mul), host64(res), "views")
+    assert (buf[0, :, 0] == 7).all() and (buf[0, :, n + 1:] == 7).all()
+    assert (buf[1, :, :3] == 7).all() and (buf[1, :, n + 3:] == 7).all()
+    # aligned rows with a space behind them: read and written in whole units
+    wide = torch.full((m, n + 64), 7.0, device="cuda").to(mul.dtype)
+    mx.linear_fused("fprop", qa, qb, out_dtype=dtype, activation="relu", out=wide[:, :n])
+    check_forward(wide[:, :n], None, acc, err, dtype, "relu", None, None, None, "aligned view")
+    assert (wide[:, n:] == 7).all()
+
+
+def test_accumulated_in_place(mx):
+    m, n, k = 1100, 3136, 288
+    qa, qb, acc, err = _pair(mx, 10, "wgrad", m, n, k)
+    c = _rows(11, (m, n), "f32")
+    before = host64(c)
+    for _ in range(2):
+        mx.linear_fused("wgrad", qa, qb, out_dtype="f32", residual=c, out=c)
+    check(c, before + 2 * acc, 2 * err + 2.0 ** -24 * (np.abs(before) + np.abs(before + acc)), "f32",
+          "accumulated")
+
+
+def test_special_values(mx):
+    """Infinities and NaN in the epilogue's inputs stay in their columns."""
+    import torch
+    m, n, k = 1030, 3200, 64
+    qa, qb, acc, err = _pair(mx, 15, "fprop", m, n, k)
+    qg, qw, gacc, gerr = _pair(mx, 15, "dgrad", m, n, k)
+    bias = torch.zeros(n, device="cuda")
+    where = [3, 1010, 2020, 3030, 3199]
+    bias[where] = torch.tensor([float("inf"), float("-inf"), float("nan"), 1e30, -1e30], device="cuda")
+    rest = np.setdiff1d(np.arange(n), where)
+    for act in ("none", "relu", "silu", "gelu", "gelu_tanh"):
+        c = mx.linear_fused("fprop", qa, qb, bias=bias, activation=act)
+        low = float("-inf") if act == "none" else 0.0
+        assert (c[:, 3] == float("inf")).all() and (c[:, 1010] == low).all(), act
+        assert c[:, 2020].isnan().all() and (c[:, 3030] == 1e30).all(), act
+        assert (c[:, 3199] == (-1e30 if act == "none" else 0)).all(), act
+        check_forward(c[:, rest], None, acc[:, rest], err[:, rest], "f32", act, None, None, None, act)
+        dz = mx.linear_act_backward(qg, qw, bias.expand(m, n).contiguous(), act)
+        flat = 1.0 if act == "none" else 0.0
+        for col, slope in ((3, 1.0), (1010, flat), (3030, 1.0), (3199, flat)):
+            check(dz[:, col], gacc[:, col] * slope, gerr[:, col], "f32", act)
+        assert act in ("none", "relu") or dz[:, 2020].isnan().all()
+
+
+# ---- grouped ----------------------------------------------------------------
+
+RAGGED = [300, 0, 5, 213, 130, 1, 500, 64]
+GROUPS = [("fprop", RAGGED, 20, 2080, 160), ("dgrad", RAGGED, 20, 160, 2080),
+          ("wgrad", RAGGED, 20, 768, 736),
+          ("fprop", [9] * 768, 3, 96, 64), ("wgrad", [9] * 50 + [0] * 718, 0, 64, 32),   # a full table
+          ("fprop", [9] * 800, 0, 128, 64), ("dgrad", [9] * 800, 0, 64, 128),           # too many groups
+          ("fprop", [2000, 3, 2300], 9, 2304, 32)]                                       # several tiles each
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("op,sizes,spare,out,cin", GROUPS)
+def test_grouped(mx, op, sizes, spare, out, cin, dtype):
+    import torch
+    rng = np.random.Generator(np.random.PCG64(len(sizes) + out))
+    t, e = sum(sizes) + spare, len(sizes)
+    ends = torch.tensor(np.cumsum(sizes), dtype=torch.int32, device="cuda")
+    rows = lambda c: mx.quantize_grouped(to_dev(activations_bf16(rng, (t, c), outlier_frac=0.01)),  # noqa: E731
+                                         ends)
+    if op == "wgrad":
+        qa, qb = rows(out).q0, rows(cin).q0
+    else:
+        w = mx.quantize_grouped(to_dev(normal_bf16(rng, (e * out, cin), 0.05)).view(e, out, cin))
+        qa, qb = (rows(cin).q1, w.q1) if op == "fprop" else (rows(out).q1, w.q0)
+    shape = (e, out, cin) if op == "wgrad" else (t, out if op == "fprop" else cin)
+    ref = _grouped_ref(op, qa, qb, oracle.group_ranges_ref(np.cumsum(sizes), t), out, cin)
+    bias = _rows(21, (e, shape[-1]), "f32")
+    mul, res = _rows(22, shape, dtype), _rows(23, shape, dtype)
+    for b, act, u, r in ((None, "none", None, res), (bias, "silu", mul, None),
+                         (bias, "gelu_tanh", mul, res)):
+        c, pre = torch.full((2, *shape), 3.0, device="cuda").to(res.dtype)
+        mx.linear_grouped(op, qa, qb, ends, out_dtype=dtype, bias=b, activation=act, mul=u,
+                          residual=r, save_pre=pre, out=c)
+        b64, u64, r64 = host64(b), host64(u), host64(r)
+        for i, (at, acc, err) in enumerate(ref):
+            pick = lambda v: None if v is None else v[at]  # noqa: E731
+            check_forward(c[at], pre[at], acc, err, dtype, act, None if b is None else b64[i],
+                          pick(u64), pick(r64), f"group {i}")
+        if op != "wgrad":
+            assert (c[sum(sizes):] == 3).all() and (pre[sum(sizes):] == 3).all()
+    if op == "dgrad":
+        pre, mul = _rows(32, shape, dtype), _rows(33, shape, dtype)
+        for u in (None, mul):
+            c, d = torch.full((2, *shape), 3.0, device="cuda").to(pre.dtype)
+            mx.linear_act_backward(qa, qb, pre, "gelu", mul=u, ends=ends, out_dtype=dtype, out=c,
+                                   dmul=None if u is None else d)
+            p64, u64 = host64(pre), host64(u)
+            for at, acc, err in ref:
+                check_backward(c[at], d[at], acc, err, p64[at], dtype, "gelu",
+                               None if u is None else u64[at], "backward")
+            assert (c[sum(sizes):] == 3).all() and (d[sum(sizes):] == 3).all()
+
+
+def test_nan_reaches_its_own_group_only(mx):
+    import torch
+    rng = np.random.Generator(np.random.PCG64(51))
+    sizes, out, cin = [137, 240, 33, 90], 2560, 2048
+    ends = torch.tensor(np.cumsum(sizes), dtype=torch.int32, device="cuda")
+    x, dy = (to_dev(normal_bf16(rng, (520, c), 1.0)) for c in (cin, out))
+    w = to_dev(normal_bf16(rng, (4 * out, cin), 1.0)).view(4, out, cin)
+    x[138, 5], w[2, 7, 9], x[515] = float("nan"), float("inf"), float("nan")
+    qx, qdy, qw = mx.quantize_grouped(x, ends), mx.quantize_grouped(dy, ends), mx.quantize_grouped(w)
+    for op, a, b, shape, at in (("fprop", qx.q1, qw.q1, (500, out), [(138, slice(None)),
+                                                                     (slice(377, 410), 7)]),
+                                ("dgrad", qdy.q1, qw.q0, (500, cin), [(slice(377, 410), 9)]),
+                                ("wgrad", qdy.q0, qx.q0, (4, out, cin), [(1, slice(None), 5)])):
+        want = torch.zeros(shape, dtype=torch.bool, device="cuda")
+        for i in at:
+            want[i] = True
+        got = mx.linear_grouped(op, a, b, ends).isnan()
+        assert torch.equal(got if op == "wgrad" else got[:500], want), op
+
+
+def test_captured_and_replayed(mx):
+    """Graphs of grouped products with other ends and operands at each replay."""
+    import torch
+    t, out, cin = 1200, 2080, 128
+    ends = torch.zeros(6, dtype=torch.int32, device="cuda")
+    x = torch.zeros(t, cin, dtype=torch.bfloat16, device="cuda")
+    w = mx.quantize_grouped(torch.randn(6, out, cin, device="cuda").bfloat16())
+    outs = [[torch.zeros(t, out, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+            for _ in range(3)]
+
+    def step(c):
+        q = mx.quantize_grouped(x, ends)
+        mx.linear_grouped("fprop", q.q1, w.q1, ends, "bf16", activation="silu", save_pre=c[1], out=c[0])
+        return mx.linear_grouped("wgrad", mx.quantize_grouped(c[0], ends).q0, q.q0, ends)
+    step(outs[2])
+    torch.cuda.synchronize()
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            dw = step(outs[i])
+        graphs.append((g, dw))
+    for split in ([1, 1, 400, 401, 900, 1200], [200, 400, 600, 800, 1000, 1100], [0, 0, 0, 0, 1200, 1200],
+                  [0] * 6):
+        ends.copy_(torch.tensor(split))
+        x.normal_()
+        for i, (g, dw) in enumerate(graphs):
+            for c in outs[i] + outs[2]:
+                c.zero_()
+            g.replay()
+            want = step(outs[2])
+            torch.cuda.synchronize()
+            assert torch.equal(dw, want), (split, i)
+            assert all(torch.equal(a, b) for a, b in zip(outs[i], outs[2])), (split, i)
