@@ -651,8 +651,8 @@ typedef struct mx_grouped_source {
  * Byte sizes of the operands that mx_quantize_grouped writes: axis 1, or
  * MX_AXIS_GROUPED. Host-only.
  * Errors: MX_ERR_NULL, MX_ERR_ARG (axis, groups < 1), MX_ERR_SHAPE (negative
- * extents, cols % 32, rows != groups * group_rows), MX_ERR_UNSUPPORTED (more
- * than 65536 groups, extents above 2^31).
+ * extents, cols % 32 for axis 1, rows != groups * group_rows),
+ * MX_ERR_UNSUPPORTED (more than 65536 groups, extents above 2^31).
  */
 mx_status mx_quantize_grouped_sizes(int64_t rows, int64_t cols, int32_t groups,
                                     int64_t group_rows, int32_t axis, size_t *codes_bytes,

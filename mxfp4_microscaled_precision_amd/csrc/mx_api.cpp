@@ -857,7 +857,7 @@ static mx_status grouped_sizes(int64_t rows, int64_t cols, int32_t groups, int64
   if (axis != 1 && axis != MX_AXIS_GROUPED) return MX_ERR_ARG;
   const mx_status st = check_groups(rows, groups, group_rows);
   if (st != MX_OK) return st;
-  if (cols < 0 || cols % 32 != 0) return MX_ERR_SHAPE;
+  if (cols < 0 || (axis == 1 && cols % 32 != 0)) return MX_ERR_SHAPE;
   if (cols > kMaxExtent) return MX_ERR_UNSUPPORTED;
   int64_t mnp, kp;
   grouped_extents(rows, cols, groups, group_rows, axis, &mnp, &kp);

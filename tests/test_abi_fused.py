@@ -147,7 +147,8 @@ def test_sizes(lib):
     assert mx.quantize_grouped_sizes(300, 96, 3) == (256 * 128 * 5 // 2, 256 * 128 * 5 // 32)
     assert mx.quantize_grouped_sizes(600, 96, 3, 200) == (256 * 128 * 6 // 2, 256 * 128 * 6 // 32)
     assert mx.quantize_grouped_sizes(0, 96, 3) == (0, 0)
-    for args, want in [((64, 48, 4), -2), ((-1, 64, 4), -2), ((64, 64, 0), -4), ((64, 64, 4, -2), -4),
+    assert mx.quantize_grouped_sizes(300, 83, 3) == mx.quantize_grouped_sizes(300, 96, 3)
+    for args, want in [((64, 48, 4, -1, 1), -2), ((-1, 64, 4), -2), ((64, 64, 0), -4), ((64, 64, 4, -2), -4),
                        ((64, 64, 4, 15), -2), ((64, 64, 4, 16, 0), -4), ((64, 64, 65537), -6),
                        ((1 << 32, 64, 4), -6)]:
         with pytest.raises(mx.MxError) as ei:

@@ -170,6 +170,32 @@ def test_grouped(mx, op, sizes, spare, out, cin, dtype):
             assert (c[sum(sizes):] == 3).all() and (d[sum(sizes):] == 3).all()
 
 
+@pytest.mark.parametrize("out,cin", [(96, 64), (832, 736)])
+def test_odd_widths(mx, out, cin):
+    """Widths that no quantizer's blocks have along a row: the same operands,
+    said to be narrower, give the same columns and write nothing beside them."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(out)
+    sizes = [9, 0, 200, 40, 60, 70, 81]
+    t, e = sum(sizes) + 5, len(sizes)
+    ends = torch.tensor(np.cumsum(sizes), dtype=torch.int32, device="cuda")
+    new = lambda *s: torch.randn(s, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    qx, qdy = mx.quantize_grouped(new(t, cin), ends), mx.quantize_grouped(new(t, out), ends)
+    qw = mx.quantize_grouped(new(e, out, cin))
+
+    def cut(q, rows, cols, **more):
+        return mx.packed_operand(q.codes, q.scales, rows, cols, 0, groups=e, **more)
+    o, c = out - 13, cin - 31
+    want = mx.linear_grouped("wgrad", qdy.q0, qx.q0, ends)
+    got = mx.linear_grouped("wgrad", cut(qdy.q0, t, o), cut(qx.q0, t, c), ends)
+    assert torch.equal(got, want[:, :o, :c])
+    want = mx.linear_grouped("dgrad", qdy.q1, qw.q0, ends)[:t - 5]
+    wide = torch.full((t, cin), 5.0, device="cuda")
+    mx.linear_grouped("dgrad", qdy.q1, cut(qw.q0, e * out, c, group_rows=out), ends, out=wide[:, :c])
+    assert torch.equal(wide[:t - 5, :c], want[:, :c])
+    assert (wide[:, c:] == 5).all() and (wide[t - 5:] == 5).all()
+
+
 def test_nan_reaches_its_own_group_only(mx):
     import torch
     rng = np.random.Generator(np.random.PCG64(51))
