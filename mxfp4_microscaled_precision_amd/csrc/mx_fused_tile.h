@@ -314,22 +314,35 @@ struct Rows {
   }
 };
 
+// Lanes 8 .. 15 of each 16 in `a` and lanes 0 .. 7 of each in `b` change places.
+__device__ __forceinline__ void swap_halves(float &a, float &b) {
+  const int x = (int)f_bits(a), y = (int)f_bits(b);
+  a = bits_f((uint32_t)__builtin_amdgcn_update_dpp(x, y, 0x128, 0xF, 0xC, false));
+  b = bits_f((uint32_t)__builtin_amdgcn_update_dpp(y, x, 0x128, 0xF, 0x3, false));
+}
+
 // The wave's part of a finished tile, 16-byte accesses, from the registers that
 // hold it: no LDS, no waits between the waves.
 //
-// Lane (lr, lg) holds columns 16 j + 4 lg .. + 3 of row lr of each strip, j < 4:
-// for fp32 that is a unit of 16 bytes, and four lanes access 64 adjacent bytes.
-// For bf16 the odd and even 16-lane rows of two neighbouring j are swapped, after
-// which the lane has eight adjacent columns, 32 p + 16 (lg % 2) + 8 (lg / 2) .. of
-// pair p: eight instructions a strip, where staging rows of 64 columns in LDS took
-// some 260 and most of the epilogue's time.
+// Lane (lr, lg) holds columns 16 j + 4 lg .. + 3 of row lr of each strip, j < 4,
+// for fp32 a unit of 16 bytes. For bf16 the odd and even 16-lane rows of two
+// neighbouring j are swapped, after which the lane has eight adjacent columns,
+// 32 p + 16 (lg % 2) + 8 (lg / 2) .. of pair p: eight instructions a strip, where
+// staging rows of 64 columns in LDS took some 260 and most of the epilogue's time.
+// An access is then 64 bytes of 16 rows. With LINES the upper eight rows of one
+// unit and the lower eight of the next change places first, 24 instructions a
+// strip, and it is 128 bytes, a line, of eight rows: worth it where three or four
+// matrices are read and written (8192x8192x2048, us without and with: fp32 with
+// mul and residual 268 -> 234, with mul and pre 306 -> 274; gradients with dmul
+// fp32 328 -> 310, bf16 206 -> 196), and not elsewhere (gradients alone fp32
+// 197 -> 199, bf16 122 -> 124; experts' bf16 rows with mul 205 -> 213).
 //
 // mul, the residual or pre of a unit are asked for one unit ahead at first, and
 // further once the accumulators of finished units leave registers for them; each
 // request goes out before its unit's stores, so that no load waits for a store.
 template <int F32, int MODE, int ACT>
 __device__ __forceinline__ void finish_rows(const FusedArgs &g, const Tile &t,
-                                            const v4f (&acc)[kRows][4], const float *columns,
+                                            v4f (&acc)[kRows][4], const float *columns,
                                             int64_t c_row, int row0, int col0, int live, int lane) {
   constexpr bool GRAD = is_gradient(MODE);
   constexpr int kSize = F32 ? 4 : 2, n = kUnit<F32>;
@@ -337,6 +350,7 @@ __device__ __forceinline__ void finish_rows(const FusedArgs &g, const Tile &t,
   constexpr int kUnits = kPerStrip * kRows;
   // two matrices to read, or one (which a forward call chooses)
   constexpr bool TWO = MODE == kForwardBoth || MODE == kGradientMul;
+  constexpr bool LINES = F32 ? MODE != kGradient : MODE == kGradientMul;
   const bool gate = !GRAD && g.e.mul;
   const Rows pm(TWO ? g.e.mul : nullptr, g.e.ldmul, c_row + row0, col0, kSize);
   const Rows po(!TWO && gate ? g.e.mul : other_of<GRAD>(g.e),
@@ -347,13 +361,18 @@ __device__ __forceinline__ void finish_rows(const FusedArgs &g, const Tile &t,
   // use (the compiler would hold one register per matrix, and spill). Rows that
   // are not the tile's are outside.
   const int lg = lane >> 4;
-  const uint32_t lr = lane & 15;
-  const uint32_t c0 = (F32 ? 4 * lg : 16 * (lg & 1) + 8 * (lg >> 1)) * kSize;
+  const uint32_t lr = lane & (LINES ? 7 : 15), side = LINES ? lane >> 3 & 1 : 0;
+  const uint32_t c0 = (F32 ? 16 * side + 4 * lg : 32 * side + 16 * (lg & 1) + 8 * (lg >> 1)) * kSize;
+  // a unit's first row in the part, and its first byte in the row
+  constexpr auto row_of = [](int u) { return u / kPerStrip * 16 + (LINES ? 8 * (u & 1) : 0); };
+  constexpr auto byte_of = [](int u) {
+    return LINES ? (u % kPerStrip >> 1) * 128 : u % kPerStrip * 64;
+  };
   const int before = t.first - row0, count = t.last - t.first;
-  auto at = [&](const Rows &m, int i) {
+  auto at = [&](const Rows &m, int row) {
     uint32_t b;
     asm volatile("v_mad_u32_u24 %0, %1, %2, %3" : "=v"(b) : "v"(lr), "s"(m.pitch), "v"(c0));
-    return lr + (uint32_t)(16 * i - before) < (uint32_t)count ? b : kOutside;
+    return lr + (uint32_t)(row - before) < (uint32_t)count ? b : kOutside;
   };
   // the last unit asked for when unit u is done: kMost units ahead at most
   constexpr int kMost = TWO ? 4 : 10, kSlots = kMost + 1;
@@ -366,15 +385,27 @@ __device__ __forceinline__ void finish_rows(const FusedArgs &g, const Tile &t,
   row_u32x4 mul[TWO ? kSlots : 1], other[kSlots];
   auto load = [&](auto unit) {
     constexpr int u = unit();
-    constexpr int i = u / kPerStrip, byte = (u % kPerStrip) * 64;
+    constexpr int i = u / kPerStrip, row = row_of(u), byte = byte_of(u);
     if (u >= kUnits || i >= live) return;
-    if constexpr (TWO) mul[u % kSlots] = pm.load(at(pm, i), 16 * i, byte);
-    if (TWO || GRAD || po.any) other[u % kSlots] = po.load(at(po, i), 16 * i, byte);
+    if constexpr (TWO) mul[u % kSlots] = pm.load(at(pm, row), row, byte);
+    if (TWO || GRAD || po.any) other[u % kSlots] = po.load(at(po, row), row, byte);
   };
   load(std::integral_constant<int, 0>());
   for_each_int<kUnits>([&](auto unit) {
     constexpr int u = unit(), i = u / kPerStrip, q = u % kPerStrip;
+    constexpr int row = row_of(u), byte = byte_of(u);
     if (i < live) {
+      if constexpr (LINES && q % 2 == 0) {
+#pragma unroll
+        for (int j = 0; j < (F32 ? 1 : 2); ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float a = acc[i][q + j][k], b = acc[i][q + j + (F32 ? 1 : 2)][k];
+            swap_halves(a, b);
+            acc[i][q + j][k] = a;
+            acc[i][q + j + (F32 ? 1 : 2)][k] = b;
+          }
+      }
       float v[n];
       if constexpr (F32) {
 #pragma unroll
@@ -391,7 +422,7 @@ __device__ __forceinline__ void finish_rows(const FusedArgs &g, const Tile &t,
       if (!GRAD && g.e.bias) {
 #pragma unroll
         for (int k = 0; k < n; k += 4) {
-          const v4f b = *reinterpret_cast<const v4f *>(columns + c0 / kSize + q * (64 / kSize) + k);
+          const v4f b = *reinterpret_cast<const v4f *>(columns + (c0 + byte) / kSize + k);
 #pragma unroll
           for (int h = 0; h < 4; ++h) v[k + h] += b[h];
         }
@@ -404,11 +435,10 @@ __device__ __forceinline__ void finish_rows(const FusedArgs &g, const Tile &t,
       constexpr int done = u == 0 ? 0 : requested(u - 1), more = requested(u) - done;
       load(std::integral_constant<int, done + 1>());
       if constexpr (more > 1) load(std::integral_constant<int, done + 2>());
-      constexpr int byte = q * 64;
       // (a store into no matrix does nothing; a branch around it would move what
       // it stores behind it, and hold every element's exponential up to there)
-      if (GRAD ? MODE == kGradientMul : p2.any) p2.store(second, at(p2, i), 16 * i, byte);
-      pc.store(c, at(pc, i), 16 * i, byte);
+      if (GRAD ? MODE == kGradientMul : p2.any) p2.store(second, at(p2, row), row, byte);
+      pc.store(c, at(pc, row), row, byte);
       __builtin_amdgcn_sched_barrier(0);
     }
   });
@@ -463,8 +493,7 @@ __device__ __forceinline__ void finish_columns(const FusedArgs &g, const Tile &t
 // The wave's part of a finished tile: `live` strips of 16 rows x 64 columns. The
 // bias of its columns waits in LDS (`columns`): eight registers less.
 template <int F32, int MODE, int ACT>
-__device__ __forceinline__ void finish(const Tile &t,
-                                       const v4f (&acc)[kRows][4], uint8_t *slab, float *columns,
+__device__ __forceinline__ void finish(const Tile &t, v4f (&acc)[kRows][4], uint8_t *slab, float *columns,
                                        int row0, int col0, int live, int lane) {
   const FusedArgs &g = read_again();
   if (live == 0 || col0 >= g.N || col0 + 64 <= 0) return;
