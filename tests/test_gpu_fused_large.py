@@ -250,3 +250,61 @@ def test_captured_and_replayed(mx):
             torch.cuda.synchronize()
             assert torch.equal(dw, want), (split, i)
             assert all(torch.equal(a, b) for a, b in zip(outs[i], outs[2])), (split, i)
+
+
+# ---- offsets past 31 and 32 bits ----------------------------------------------
+
+@pytest.mark.parametrize("op,dtype", [("fprop", "bf16"), ("dgrad", "f32")])
+def test_offsets_of_large_outputs(mx, op, dtype):
+    """4.6 and 9.2 GB of output, in tiles: A's rows repeat every 256, so C's do."""
+    import torch
+    m, n, k = 70144, 32768, 32
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(256, k, generator=gen, device="cuda").bfloat16()
+    w = torch.randn((n, k) if op == "fprop" else (k, n), generator=gen, device="cuda").bfloat16()
+    qb = mx.quantize(w, 1 if op == "fprop" else 0)
+    qa = mx.quantize(x.repeat(m // 256, 1), 1)
+    acc, err = product(values(mx.quantize(x, 1)), values(qb))
+    c = mx.linear_fused(op, qa, qb, out_dtype=dtype, activation="relu")
+    check_forward(c[:256], None, acc, err, dtype, "relu", None, None, None, op)
+    for i in range(0, m, 256 * 8):
+        part = c[i:i + 256 * 8].view(-1, 256, n)
+        assert (part == c[:256]).all(), i
+    if op == "fprop":                            # a handful of rows a group: the few-rows kernel
+        e = 11
+        ends = torch.arange(1, e + 1, dtype=torch.int32, device="cuda") * 7
+        big = torch.empty(1 << 32, dtype=torch.bfloat16, device="cuda").view(128, -1)
+        out = big[:77, -n:]                      # rows 64 MB apart, 4.3 GB to the last
+        qw = mx.packed_operand(qb.codes, qb.scales, n, k, 1, groups=1, group_rows=n)
+        mx.linear_grouped("fprop", mx.quantize(x[:77], 1), qw, ends[-1:], out_dtype="bf16", out=out)
+        check_forward(out, None, acc[:77], err[:77], "bf16", "none", None, None, None, "few rows")
+
+
+def test_rows_far_apart(mx):
+    """Rows of C, mul and the residual 17 MB apart (read and written by columns)."""
+    import torch
+    m, n, k = 1100, 3920, 96
+    qa, qb, acc, err = _pair(mx, 4, "fprop", m, n, k)
+    far = torch.empty(m * (1 << 23) + (1 << 20), dtype=torch.bfloat16, device="cuda")
+    views = [far.as_strided((m, n), (1 << 23, 1), 5000 * i) for i in range(3)]
+    mul, res = _rows(2, (m, n), "bf16"), _rows(3, (m, n), "bf16")
+    views[0].copy_(mul)
+    views[1].copy_(res)
+    mx.linear_fused("fprop", qa, qb, out_dtype="bf16", activation="silu", mul=views[0],
+                    residual=views[1], out=views[2])
+    check_forward(views[2], None, acc, err, "bf16", "silu", None, host64(mul), host64(res), "far")
+    assert torch.equal(views[0], mul) and torch.equal(views[1], res)
+
+
+def test_offsets_of_a_large_quantizer_source(mx):
+    """3.9 GB of rows, through an index too: the ordinary quantizer's bytes."""
+    import torch
+    t, c = 60416, 32768
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(t, c, generator=gen, device="cuda", dtype=torch.bfloat16)
+    ends = torch.tensor([t], dtype=torch.int32, device="cuda")
+    want = [mx.quantize(x, a) for a in (1, 0)]
+    for index in (None, torch.arange(t, device="cuda")):
+        q = mx.quantize_grouped(x, ends, index=index)
+        for got, ref in zip((q.q1, q.q0), want):
+            assert torch.equal(got.codes, ref.codes) and torch.equal(got.scales, ref.scales)
