@@ -917,10 +917,8 @@ static mx_status fill_epilogue(const mx_epilogue *e, void *C, int64_t rows, int6
     const mx_status st = empty ? MX_OK : check_matrix(m[i].p, rows, N, m[i].ld, dtype);
     if (st != MX_OK) return st;
     if (m[i].p == nullptr) continue;
-    // 16-byte accesses; the offsets of 128 rows stay below 2^31 bytes
-    if (!aligned(m[i].p, 16) || m[i].ld * dtype_size(dtype) % 16 != 0 ||
-        m[i].ld * dtype_size(dtype) >= (int64_t)1 << 24)
-      vec = 0;
+    // the offsets of 128 rows stay below 2^31 bytes
+    if (m[i].ld * dtype_size(dtype) >= (int64_t)1 << 24) vec = 0;
     for (int j = 0; j < i && !empty; ++j) {
       if (m[j].p != m[i].p) continue;
       if (m[i].out && m[j].out) return MX_ERR_ARG;

@@ -235,31 +235,31 @@ __device__ __forceinline__ int64_t other_ld(const EpiArgs &e) {
   return GRAD ? e.ldpre : e.ldres;
 }
 
-// One element as stored, into element i of eight, and back.
+// Eight consecutive columns of a row, from any element on: gfx950 loads and stores
+// 16 bytes at any alignment.
+typedef uint32_t any_row_u32x4 __attribute__((ext_vector_type(4), aligned(2)));
 template <int F32>
-__device__ __forceinline__ uint32_t load_bits(const void *p, int64_t at) {
-  return F32 ? static_cast<const uint32_t *>(p)[at] : static_cast<const uint16_t *>(p)[at];
+__device__ __forceinline__ Row8<F32> load_row8(const void *p, int64_t at) {
+  const any_row_u32x4 *from = reinterpret_cast<const any_row_u32x4 *>(
+      static_cast<const uint8_t *>(p) + at * (F32 ? 4 : 2));
+  Row8<F32> r;
+#pragma unroll
+  for (int k = 0; k < (F32 ? 2 : 1); ++k) r.w[k] = from[k];
+  return r;
 }
 template <int F32>
-__device__ __forceinline__ void put_bits(Row8<F32> &r, int i, uint32_t bits) {
-  if constexpr (F32)
-    r.w[i >> 2][i & 3] = bits;
-  else
-    r.w[0][i >> 1] = i & 1 ? r.w[0][i >> 1] | bits << 16 : bits;      // even elements first
-}
-template <int F32>
-__device__ __forceinline__ void store_bits(void *p, int64_t at, const Row8<F32> &r, int i) {
-  if constexpr (F32)
-    static_cast<uint32_t *>(p)[at] = r.w[i >> 2][i & 3];
-  else
-    static_cast<uint16_t *>(p)[at] = (uint16_t)(r.w[0][i >> 1] >> (16 * (i & 1)));
+__device__ __forceinline__ void store_row8(void *p, int64_t at, const Row8<F32> &r) {
+  any_row_u32x4 *to =
+      reinterpret_cast<any_row_u32x4 *>(static_cast<uint8_t *>(p) + at * (F32 ? 4 : 2));
+#pragma unroll
+  for (int k = 0; k < (F32 ? 2 : 1); ++k) to[k] = r.w[k];
 }
 
 // One element, widened, and back.
 template <int F32>
 __device__ __forceinline__ float load_one(const void *p, int64_t at) {
-  const uint32_t b = load_bits<F32>(p, at);
-  return bits_f(F32 ? b : b << 16);
+  return F32 ? static_cast<const float *>(p)[at]
+             : bits_f((uint32_t) static_cast<const uint16_t *>(p)[at] << 16);
 }
 template <int F32>
 __device__ __forceinline__ void store_one(void *p, int64_t at, float v) {
@@ -273,29 +273,6 @@ __device__ __forceinline__ void store_one(void *p, int64_t at, float v) {
 __device__ __forceinline__ float load_bias(const EpiArgs &e, int64_t at) {
   return e.bias_f32 ? static_cast<const float *>(e.bias)[at]
                     : bits_f((uint32_t) static_cast<const uint16_t *>(e.bias)[at] << 16);
-}
-
-// Eight consecutive columns of a row, from element `at` on: `vec` as one
-// access, else those in [lo, hi) one by one.
-template <int F32>
-__device__ __forceinline__ Row8<F32> load_cols(const void *p, int64_t at, bool vec, int lo,
-                                               int hi) {
-  if (vec) return load8<F32>(p, at);
-  Row8<F32> r;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) put_bits(r, i, i >= lo && i < hi ? load_bits<F32>(p, at + i) : 0u);
-  return r;
-}
-template <int F32>
-__device__ __forceinline__ void store_cols(void *p, int64_t at, bool vec, int lo, int hi,
-                                           const Row8<F32> &r) {
-  if (vec) {
-    store8<F32>(p, at, r);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i >= lo && i < hi) store_bits<F32>(p, at + i, r, i);
 }
 
 }  // namespace mx

@@ -148,8 +148,8 @@ __global__ __launch_bounds__(64 * kWaves) void fused_small_kernel(FusedArgs g, i
       if (r >= kRows || row < first || row >= last) continue;
       const int64_t at = c_row + row;
       Row8<F32> mul, other, c, second;
-      if (g.e.mul) mul = load8<F32>(g.e.mul, at * g.e.ldmul + col);
-      if (other_of<GRAD>(g.e)) other = load8<F32>(other_of<GRAD>(g.e), at * other_ld<GRAD>(g.e) + col);
+      if (g.e.mul) mul = load_row8<F32>(g.e.mul, at * g.e.ldmul + col);
+      if (other_of<GRAD>(g.e)) other = load_row8<F32>(other_of<GRAD>(g.e), at * other_ld<GRAD>(g.e) + col);
       float v[8], bias[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -168,8 +168,8 @@ __global__ __launch_bounds__(64 * kWaves) void fused_small_kernel(FusedArgs g, i
       with_act(g.e.act, [&](auto act) {
         epilogue8<F32, GRAD, act()>(v, bias, g.e.mul, g.e.residual, mul, other, c, second);
       });
-      if (second_of<GRAD>(g.e)) store8<F32>(second_of<GRAD>(g.e), at * second_ld<GRAD>(g.e) + col, second);
-      store8<F32>(g.c, at * g.ldc + col, c);
+      if (second_of<GRAD>(g.e)) store_row8<F32>(second_of<GRAD>(g.e), at * second_ld<GRAD>(g.e) + col, second);
+      store_row8<F32>(g.c, at * g.ldc + col, c);
     }
     return;
   }

@@ -20,8 +20,8 @@
 //    would fill at most half of the compute units.
 //  * K is a tile's own: a slice range of either operand, which may be empty.
 //  * The epilogue (mx_epilogue.h) works on the registers that hold the sums, 16
-//    bytes a lane and access, or by columns through LDS where a matrix's rows are
-//    not 16-byte aligned.
+//    bytes a lane and access (at any alignment), or by columns through LDS in the
+//    64 columns where the matrix ends, and where its rows are 16 MB or more apart.
 //
 // Bound by two things one after the other: the stages by the matrix instructions
 // (8192x14336x4096 alone: 201 us, 4.8 PFLOP/s, what the card's power allows), the
@@ -459,7 +459,7 @@ __device__ __forceinline__ void finish_rows(const FusedArgs &g, const Tile &t,
   });
 }
 
-// The same element by element, for matrices that do not take 16-byte accesses:
+// The same element by element, where 64 columns are not all the matrix's:
 // the sums go through LDS, eight rows at a time, and lane l has column l of four
 // rows at once, so that 64 lanes still access 64 adjacent columns.
 template <int F32, int MODE, int ACT>

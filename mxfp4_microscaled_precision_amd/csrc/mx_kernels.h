@@ -106,7 +106,7 @@ struct EpiArgs {
   void *dmul;
   int64_t ldmul, ldres, ldpre, lddmul;
   int bias_f32, act;
-  int vec;                         // every matrix (C too) takes 16-byte accesses at columns 8 i
+  int vec;                         // 128 rows of any matrix (C too) have 32-bit offsets
 };
 
 enum { MX_K_FPROP = 0, MX_K_DGRAD = 1, MX_K_WGRAD = 2 };

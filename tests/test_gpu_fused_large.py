@@ -1,6 +1,7 @@
 """Products with an epilogue and grouped ones, of sizes with enough 64x64 tiles
-(more than three a compute unit) for the kernel of 256x256 tiles: tiles cut by
-the matrix's ends, halves of tiles, several tiles a workgroup, matrices read and
+(more than three a compute unit, and columns in multiples of 64 or more than 160
+GFLOP) for the kernel of 256x256 tiles, and beside those limits: tiles cut by the
+matrix's ends, halves of tiles, several tiles a workgroup, matrices read and
 written by columns, groups that end inside a tile. Against fp64."""
 import numpy as np
 import pytest
@@ -14,13 +15,13 @@ from test_gpu_fused import _grouped_ref, _pair, _rows
 pytestmark = pytest.mark.gpu
 
 # N of whole 16-byte units, of 4-element ones only (fp32: whole, bf16: not), odd
-SHAPES = [(1100, 3136, 160), (1290, 3204, 96), (1100, 3905, 288)]
+SHAPES = [(1100, 3136, 160), (1290, 3204, 96), (1100, 3905, 288), (1290, 3200, 96), (1100, 3904, 288)]
 WAYS = [("none", "b"), ("relu", "bm"), ("silu", "br"), ("gelu", "mr"), ("gelu_tanh", "bmr"),
         ("silu", "m"), ("none", "r"), ("gelu", "")]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("shape,op", zip(SHAPES, ["fprop", "dgrad", "wgrad"]))
+@pytest.mark.parametrize("shape,op", zip(SHAPES, ["fprop", "dgrad", "wgrad", "dgrad", "wgrad"]))
 def test_forward(mx, shape, op, dtype):
     m, n, k = shape
     qa, qb, acc, err = _pair(mx, m + n, op, m, n, k)
@@ -61,10 +62,11 @@ def test_several_tiles_a_workgroup(mx, op, act):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-def test_strided_and_misaligned_matrices(mx, dtype):
+@pytest.mark.parametrize("n", [3600, 3648])
+def test_strided_and_misaligned_matrices(mx, n, dtype):
     """Row-strided views at odd addresses; what lies between the rows stays."""
     import torch
-    m, n, k = 1250, 3600, 160
+    m, k = 1250, 160
     qa, qb, acc, err = _pair(mx, 9, "fprop", m, n, k)
     mul, res = _rows(6, (m, n), dtype, n + 9), _rows(7, (m, n), dtype, n + 3)
     bias = _rows(8, (n + 1,), "bf16")[1:]
@@ -117,11 +119,48 @@ def test_special_values(mx):
         assert act in ("none", "relu") or dz[:, 2020].isnan().all()
 
 
+def test_ends_inside_a_tile(mx):
+    """More than 160 GFLOP: the tile kernel's last columns, odd rows apart."""
+    import torch
+    m, n, k = 4224, 4331, 4608
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    new = lambda *s: torch.randn(s, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    qa, qb, qw = mx.quantize(new(m, k), 1), mx.quantize(new(n, k), 1), mx.quantize(new(k, n), 0)
+    va, vb, vw = (torch.tensor(values(q), device="cuda") for q in (qa, qb, qw))
+
+    def exact(v):
+        return ((va @ v.T).cpu().numpy(),
+                ((k / 128 + 10) * 2.0 ** -22 * (va.abs() @ v.abs().T)).cpu().numpy())
+    mul, res, bias = _rows(2, (m, n), "bf16"), _rows(3, (m, n), "bf16"), _rows(4, (n,), "f32")
+    acc, err = exact(vb)
+    c, pre = mx.linear_fused("fprop", qa, qb, "bf16", bias=bias, activation="silu", mul=mul,
+                             residual=res, save_pre=True)
+    check_forward(c, pre, acc, err, "bf16", "silu", host64(bias), host64(mul), host64(res), "forward")
+    acc, err = exact(vw)
+    for u in (None, mul):
+        got = mx.linear_act_backward(qa, qw, res, "gelu", mul=u, out_dtype="bf16")
+        dz, dmul = got if u is not None else (got, None)
+        check_backward(dz, dmul, acc, err, host64(res), "bf16", "gelu", host64(u), "backward")
+    # the same by experts, whose columns begin inside the operand's tiles
+    ends = torch.tensor([1000, 1003, 4200], dtype=torch.int32, device="cuda")
+    w = new(3, n, k)
+    qw = mx.quantize_grouped(w, dual=False)
+    out = torch.full((m, n), 3.0, device="cuda")
+    mx.linear_grouped("fprop", qa, qw.q1, ends, out=out)
+    vw = torch.tensor(values(qw.q1), device="cuda").view(3, n, k)
+    for e, (lo, hi) in enumerate(((0, 1000), (1000, 1003), (1003, 4200))):
+        acc = (va[lo:hi] @ vw[e].T).cpu().numpy()
+        err = (k / 128 + 10) * 2.0 ** -22 * (va[lo:hi].abs() @ vw[e].abs().T).cpu().numpy()
+        check(out[lo:hi], acc, err, "f32", f"expert {e}")
+    assert (out[4200:] == 3).all()
+
+
 # ---- grouped ----------------------------------------------------------------
 
 RAGGED = [300, 0, 5, 213, 130, 1, 500, 64]
 GROUPS = [("fprop", RAGGED, 20, 2080, 160), ("dgrad", RAGGED, 20, 160, 2080),
-          ("wgrad", RAGGED, 20, 768, 736),
+          ("wgrad", RAGGED, 20, 768, 736), ("fprop", RAGGED, 20, 2112, 160),
+          ("dgrad", RAGGED, 20, 160, 2112), ("wgrad", RAGGED, 20, 768, 768), ("fprop", [9] * 768, 3, 128, 64),
           ("fprop", [9] * 768, 3, 96, 64), ("wgrad", [9] * 50 + [0] * 718, 0, 64, 32),   # a full table
           ("fprop", [9] * 800, 0, 128, 64), ("dgrad", [9] * 800, 0, 64, 128),           # too many groups
           ("fprop", [2000, 3, 2300], 9, 2304, 32)]                                       # several tiles each
