@@ -138,7 +138,7 @@ __global__ __launch_bounds__(64 * kWaves) void fused_small_kernel(FusedArgs g, i
 
   // A lane has eight columns of a row, where every matrix takes 16-byte accesses;
   // else one column of four rows, so that the lanes still access adjacent columns.
-  const bool vec = g.e.vec && col0 >= 0 && col0 + kCols <= g.N && (col0 & 7) == 0;
+  const bool vec = g.e.vec && col0 >= 0 && col0 + kCols <= g.N;
   if (vec) {
     constexpr int kUnits = kCols / 8, kStep = 64 / kUnits;        // rows of a wave at a time
     __syncthreads();

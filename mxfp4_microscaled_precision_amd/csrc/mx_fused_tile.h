@@ -518,7 +518,7 @@ __device__ __forceinline__ void finish(const Tile &t, v4f (&acc)[kRows][4], uint
   columns[lane] =
       g.e.bias && col >= 0 && col < g.N ? load_bias(g.e, (int64_t)t.e * g.N + col) : 0.0f;
   wave_sync();
-  const bool vec = g.e.vec && (col0 & 7) == 0 && col0 >= 0 && col0 + 64 <= g.N;
+  const bool vec = g.e.vec && col0 >= 0 && col0 + 64 <= g.N;
   if (vec)
     finish_rows<F32, MODE, ACT>(g, t, acc, columns, c_row, row0, col0, live, lane);
   else
