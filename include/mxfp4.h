@@ -573,8 +573,8 @@ typedef enum mx_activation {
  *            with mul only.
  * Matrices that are read may be C or another output itself (same pointer and
  * leading dimension: an output is then written over what it was computed from)
- * but overlap them in no other way. Alignment: their element size (16 bytes,
- * with leading dimensions of 16 bytes, is faster).
+ * but overlap them in no other way. Alignment: their element size (rows less
+ * than 16 MB apart, and N a multiple of 64 in large products, are faster).
  */
 typedef struct mx_epilogue {
   int32_t activation, gradient;
