@@ -98,7 +98,7 @@ __device__ __forceinline__ float act_both(float z, float &slope) {
   if (act == MX_K_ACT_NONE) return z;
   const float up = __builtin_elementwise_maximum(z, 0.0f);
   if (act == MX_K_ACT_RELU) {
-    slope = z > 0.0f ? 1.0f : 0.0f;
+    slope = z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;   // NaN stays NaN
     return up;
   }
   float e;                                 // slope Phi(z) + z phi(z)

@@ -33,7 +33,7 @@ def act_ref(z: np.ndarray, act: str) -> Tuple[np.ndarray, np.ndarray]:
         if act == "none":
             return z, np.ones_like(z)
         if act == "relu":
-            return np.maximum(z, 0.0), np.where(z > 0, 1.0, 0.0)
+            return np.maximum(z, 0.0), np.where(np.isnan(z), z, np.where(z > 0, 1.0, 0.0))
         if act == "gelu":
             cdf = 0.5 * (1.0 + _erf(z / np.sqrt(2.0)))
             return z * cdf, cdf + z * np.exp(-0.5 * z * z) / np.sqrt(2.0 * np.pi)
