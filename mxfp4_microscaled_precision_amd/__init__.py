@@ -898,9 +898,6 @@ def quantize_grouped_sizes(rows: int, cols: int, groups: int, group_rows: int = 
     return cb.value, sb.value
 
 
-_grouped_sizes = functools.lru_cache(maxsize=256)(quantize_grouped_sizes)
-
-
 @functools.lru_cache(maxsize=256)
 def _grouped_workspace(rows: int, cols: int, groups: int, group_rows: int) -> int:
     need = ctypes.c_size_t()
@@ -1010,9 +1007,9 @@ def quantize_grouped(x, ends=None, index=None, dual: bool = True, rotate: str = 
             src, ip = 0, None
     place, handle = _place(device, stream)
     with place:
-        size = _grouped_sizes(rows, cols, groups, each, 1)
+        size = quantize_grouped_sizes(rows, cols, groups, each, 1)
         if dual:
-            size += _grouped_sizes(rows, cols, groups, each, AXIS_GROUPED)
+            size += quantize_grouped_sizes(rows, cols, groups, each, AXIS_GROUPED)
         need = _grouped_workspace(rows, cols, groups, each) if sums else 0
         buf = [torch.empty(b, dtype=torch.uint8, device=device) for b in size]
         ptr = [b.data_ptr() or None for b in buf] + [None, None]
