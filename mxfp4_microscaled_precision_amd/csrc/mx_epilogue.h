@@ -1,14 +1,17 @@
-// What a product's epilogue computes, eight consecutive columns of one row at
-// a time, in fp32 from the accumulator to the one rounding of each output:
+// What a product's epilogue computes, in fp32 from the accumulator to the one
+// rounding of each output:
 //
 //   forward    z = acc + bias;  pre = z;  C = act(z) * mul + residual
 //   gradient   C = acc * mul * act'(pre);  dmul = acc * act(pre)
 //
-// A lane owns 8 columns of a row (16 bytes of a bf16 row, 32 of an fp32 one), so
-// mul, residual, pre and C are read and written as whole 128-byte row pieces by
-// eight lanes; where their addresses are not for 16-byte accesses the tile
-// kernel's lanes own a column of 8 rows instead, 64 lanes 64 columns. Which
-// activation it is is a wave-uniform branch.
+// mul, residual, pre and C are read and written 16 bytes at a time, at any
+// alignment: a lane of the tile kernel takes a unit (8 bf16 or 4 fp32 columns of a
+// row), one of the few-rows kernel 8 columns of a row. Where the columns of a wave's
+// part (of the few-rows kernel's workgroup) are not all the matrix's, or its rows
+// are 16 MB or more apart (EpiArgs.vec), a lane takes one column of four rows
+// instead, so that the lanes still access adjacent columns. Which activation it is
+// is a wave-uniform branch in the few-rows kernel, around all of a lane's elements;
+// the tile kernel is compiled for each.
 #pragma once
 
 #include <hip/hip_runtime.h>

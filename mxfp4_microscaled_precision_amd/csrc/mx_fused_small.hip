@@ -12,8 +12,9 @@
 // Bound by the weights' bytes where they are many, by latency elsewhere: one row
 // of 14336x4096 weights (31 MB) takes 6.7 us, 48 rows of 8 experts 4096x4096
 // (71 MB) 14.7 us, 4.9 TB/s; 1237x2081x2080 in fp32 with bias, GELU and residual
-// 20 us, 777x1056x992's gradient 7.5 us, where two rounds of workgroups each wait
-// for their operands once.
+// 20 us, 777x1056x992's gradient 7.5 us. Of more than some 64 rows it is bound by
+// this tiling: the operands are asked for once per 64x64 tile (93 MB for the first of
+// these, whose operands are 3.7 MB), two slices at a time.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -136,8 +137,9 @@ __global__ __launch_bounds__(64 * kWaves) void fused_small_kernel(FusedArgs g, i
     for (int j = 0; j < J; ++j)
       *reinterpret_cast<v4f *>(&red[wave][16 * i + lr][16 * j + 4 * lg]) = acc[i][j];
 
-  // A lane has eight columns of a row, where every matrix takes 16-byte accesses;
-  // else one column of four rows, so that the lanes still access adjacent columns.
+  // A lane has eight columns of a row where the workgroup's columns are all the
+  // matrix's (and its rows less than 16 MB apart); else one column of four rows, so
+  // that the lanes still access adjacent columns.
   const bool vec = g.e.vec && col0 >= 0 && col0 + kCols <= g.N;
   if (vec) {
     constexpr int kUnits = kCols / 8, kStep = 64 / kUnits;        // rows of a wave at a time

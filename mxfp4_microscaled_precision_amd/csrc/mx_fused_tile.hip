@@ -45,9 +45,11 @@ static hipError_t fused_tile_launch(FusedArgs g, hipStream_t stream) {
 // average: what counts is then that its weights are read once. Measured, us (few rows /
 // tiles): with SiLU, 512x4096x4096 16.6 / 22.4, 128x14336x4096 15.6 / 23.5,
 // 2048x1024x4096 12.1 / 21.9, and past the limit 1024x4096x4096 25.8 / 23.3,
-// 256x14336x4096 26.7 / 23.4; 256 rows of 8 experts 4096x4096 25.2 / 29.7, of 64
+// 256x14336x4096 26.7 / 23.4 (the plain product alone: 14.4
+// and 15.0); 256 rows of 8 experts 4096x4096 25.2 / 29.7, of 64
 // experts 2048x1024 18.3 / 21.5, 4096 rows of those 45.7 / 27.6; bf16 with a
-// residual that ends inside 64 columns, 7417x3324x160 52 / 162, 4096x4097x4096 78 / 182,
+// residual that ends inside 64 columns, 7417x3324x160 52 / 162 (with bias and SiLU as
+// well 64 / 200), 4096x4097x4096 78 / 182,
 // 8192x1056x4096 50 / 95 and without one 8192x8200x2048 (275 GFLOP) 187 / 156.
 hipError_t fused_launch(const FusedArgs &g, hipStream_t stream) {
   const bool wgrad = g.kind == MX_K_WGRAD;
