@@ -101,7 +101,7 @@ __device__ __forceinline__ float act_both(float z, float &slope) {
   if (act == MX_K_ACT_NONE) return z;
   const float up = __builtin_elementwise_maximum(z, 0.0f);
   if (act == MX_K_ACT_RELU) {
-    slope = z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;   // NaN stays NaN
+    slope = z > 0.0f ? 1.0f : up;          // (up: 0, but NaN for NaN)
     return up;
   }
   float e;                                 // slope Phi(z) + z phi(z)
